@@ -270,6 +270,67 @@ mlora_status mlora_apply_ex(mlora_pool *pool, const mlora_segments *segs, const 
 mlora_status mlora_base_gemm_apply(mlora_pool *pool, const mlora_segments *segs, const void *X, int64_t ldx,
                                    const void *W, int64_t ldw, void *Y, int64_t ldy, void *stream);
 
+/*
+ * 4-bit microscaled matrices (the OCP microscaling format MXFP4; the pages have no
+ * counterpart beyond "The dtype boundary between a quantized base model and LoRA"): a
+ * block of 32 consecutive elements of a row shares the scale 2^e,
+ * e = floor(log2(max |x|)) - 2 clamped to [-127, 127] (-127 for a block of zeros), kept as
+ * the byte e + 127; each element is x / 2^e rounded to the nearest of
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6 with its sign (ties to the even code, larger magnitudes to 6).
+ * A block that holds an infinity or a NaN has the scale byte 255 and reads back as NaN.
+ *   codes:  row r at codes + r * ld, two codes per byte (the first in the low four bits;
+ *           bit 3 of a code is the sign), ceil(n_cols / 32) * 16 bytes per row: the last
+ *           block is padded with zero codes.  ld in bytes, a multiple of 16.
+ *   scales: tiles of 128 rows x 4 blocks, 512 bytes each; tile (r / 128, b / 4) is at
+ *           ((r / 128) * 2 * ceil(n_cols / 256) + b / 4) * 512, and row r's block b in it at
+ *           (r % 32) * 16 + (r % 128 / 32) * 4 + b % 4.  mlora_mx_scale_bytes bytes; entries
+ *           past the last block of a row are 0, entries of rows past n_rows are not used.
+ * codes and scales are device memory of the caller, 16-byte aligned; n_cols is a multiple
+ * of 8.  An empty matrix (n_rows 0) needs neither.
+ */
+typedef struct {
+    int32_t n_rows, n_cols;
+    int64_t ld;
+    void *codes;
+    void *scales;
+} mlora_mx_matrix;
+
+/* Bytes of the scales of an n_rows x n_cols matrix (-1 for a negative size). */
+int64_t mlora_mx_scale_bytes(int32_t n_rows, int32_t n_cols);
+
+/*
+ * Quantise X (device, bf16, fp16 or fp32 as x_dtype says, [Q->n_rows, Q->n_cols], row
+ * stride ldx elements, rows and strides of whole 16-byte vectors) into Q, on the current
+ * device: activations before a 4-bit projection, or weights once when they are loaded.
+ * MLORA_ERR_UNSUPPORTED if n_cols is no multiple of 8.
+ */
+mlora_status mlora_mx_quantize(const void *X, int32_t x_dtype, int64_t ldx, const mlora_mx_matrix *Q, void *stream);
+
+/* The values Q stands for, rounded once to x_dtype (exact in fp32, and in bf16). */
+mlora_status mlora_mx_dequantize(const mlora_mx_matrix *Q, void *X, int32_t x_dtype, int64_t ldx, void *stream);
+
+/*
+ * The base projection of a 4-bit model and the LoRA delta in one pass, as
+ * mlora_base_gemm_apply has it for a bf16 one:
+ *
+ *   Y[t, :] = round(Xq[t, :] W^T + s_g (X[t, :] A_a^T) B_a^T)   rows t of adapter segments
+ *   Y[t, :] = round(Xq[t, :] W^T)                                every other row
+ *
+ * Xq [n_rows, d_in] and W [d_out, d_in] are 4-bit matrices, multiplied as they are by the
+ * tensor core (the codes' products are exact) and summed in fp32; the LoRA branch reads the
+ * activations X from before the quantisation (bf16 [n_rows, d_in], row stride ldx), as
+ * mlora_base_gemm_apply does, and the sum is rounded once to y_dtype (MLORA_DTYPE_BF16,
+ * _FP16 or _FP32).  Y [n_rows, d_out], row stride ldy, is written for every row and never
+ * read.  Xq is the caller's, so that projections that share X (q/k/v, gate/up) quantise it
+ * once.  segs may be NULL: base projection only, for a module without adapters; X is then
+ * not read and may be NULL.  Errors, rejected segments and the workspace as
+ * mlora_base_gemm_apply; also MLORA_ERR_INVALID_ARG where a matrix does not match the
+ * pool's d_in and d_out, or segs->n_rows is not Xq's.
+ */
+mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, const void *X, int64_t ldx,
+                                 const mlora_mx_matrix *Xq, const mlora_mx_matrix *W, void *Y, int32_t y_dtype,
+                                 int64_t ldy, void *stream);
+
 /* Projections one mlora_apply_multi call may cover. */
 #define MLORA_MAX_FUSED 4
 
@@ -353,6 +414,73 @@ mlora_status mlora_build_segments(const int32_t *row_slots, int32_t n_rows,
                                   int32_t *offsets, int32_t *slots, int32_t *token_indices,
                                   int32_t *n_segments, int32_t *max_segment_rows,
                                   const mlora_pool *pool, int32_t *ranks);
+
+/*
+ * Rows grouped by slot on the device, for batches whose slots the host does not know: a
+ * router's choices, or a step captured into a graph (mlora_build_segments is a host call).
+ * Entry e = t * top_k + j of row_slots (device, int32 [n_rows, top_k]) is row t's j-th slot,
+ * -1 for the base model; N = n_rows * top_k entries are sorted by slot, stably.  The outputs
+ * are device arrays the caller sizes with S = min(n_slots + 1, N):
+ *   offsets   [S + 1]  the grouped positions of the segments
+ *   slots     [S]      the slots with entries in ascending order (base, -1, first), then
+ *                      -1 for the remaining, empty segments
+ *   ranks     [S]      the slots' ranks (0 for base), or NULL
+ *   order     [N]      grouped position -> entry
+ *   positions [N]      entry -> grouped position
+ * With top_k = 1 they are a mlora_segments as it stands (n_segments S, n_tokens N,
+ * token_indices = order).  With more, mlora_gather_rows brings the rows into grouped order
+ * first, where the segments' rows are consecutive (token_indices NULL, n_rows = N).
+ * An entry that is no slot of the pool (< -1 or >= n_slots) is in no segment: its position
+ * is -1, order lists it behind offsets[S], and MLORA_FLAG_BAD_SLOT is set.
+ * MLORA_ERR_UNSUPPORTED for a pool of more than 12798 slots.
+ */
+typedef struct {
+    int32_t *offsets;
+    int32_t *slots;
+    int32_t *ranks;
+    int32_t *order;
+    int32_t *positions;
+} mlora_row_groups;
+
+mlora_status mlora_group_rows(mlora_pool *pool, const int32_t *row_slots, int32_t n_rows, int32_t top_k,
+                              const mlora_row_groups *out, void *stream);
+
+/*
+ * The rows in grouped order: Xs[positions[t * top_k + j], :] = X[t, :].  X: device
+ * [n_rows, d] and Xs: device [n_tokens, d], both of `dtype` (MLORA_DTYPE_BF16, _FP16 or
+ * _FP32), row strides ldx and ldxs elements; rows and strides are whole 16-byte vectors
+ * (MLORA_ERR_UNSUPPORTED for a d that is not) and 16-byte aligned.  Rows of Xs that no
+ * position names are left as they were; a position of -1 is skipped, any other outside
+ * [0, n_tokens) is skipped and flagged MLORA_FLAG_BAD_ROW in the pool.  The gradient of X is
+ * mlora_combine_rows of the gradient of Xs, without weights.
+ */
+mlora_status mlora_gather_rows(mlora_pool *pool, const int32_t *positions, int32_t n_rows, int32_t top_k, const void *X,
+                               int64_t ldx, int32_t dtype, int32_t d, int32_t n_tokens, void *Xs, int64_t ldxs,
+                               void *stream);
+
+/*
+ * And back: Y[t, :] = sum_j weights[t, j] Ys[positions[t * top_k + j], :], summed in fp32 in
+ * the order of j and rounded once.  weights: device fp32 [n_rows, top_k], or NULL for ones.
+ * Every row of Y is written (zeros where all its positions are -1); Y must not overlap Ys.
+ * Types, strides and positions as mlora_gather_rows.
+ */
+mlora_status mlora_combine_rows(mlora_pool *pool, const int32_t *positions, const float *weights, int32_t n_rows,
+                                int32_t top_k, const void *Ys, int64_t ldys, int32_t dtype, int32_t d,
+                                int32_t n_tokens, void *Y, int64_t ldy, void *stream);
+
+/*
+ * The gradients of mlora_combine_rows from dY, the gradient of Y:
+ *   dYs[positions[t * top_k + j], :] = weights[t, j] dY[t, :]
+ *   dweights[t, j] = sum_c dY[t, c] Ys[positions[t * top_k + j], c]     (0 for position -1)
+ * dYs may be NULL (not computed), dweights may be NULL (Ys is then not read and may be
+ * NULL), not both.  dYs must not overlap dY or Ys; its rows that no position names are left as they
+ * were.  dweights: device fp32 [n_rows, top_k], summed in fp32 in a fixed order.  Where two
+ * entries name one position (group_rows makes none), that row of dYs gets one of their values.
+ */
+mlora_status mlora_combine_rows_backward(mlora_pool *pool, const int32_t *positions, const float *weights,
+                                         int32_t n_rows, int32_t top_k, const void *dY, int64_t lddy, const void *Ys,
+                                         int64_t ldys, int32_t dtype, int32_t d, int32_t n_tokens, void *dYs,
+                                         int64_t lddys, float *dweights, void *stream);
 
 /*
  * Host-side adapter cache over the slots of a pool: which adapter (a caller-chosen

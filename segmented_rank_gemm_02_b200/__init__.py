@@ -35,6 +35,8 @@ EXPORTS = ("mlora_pool_create", "mlora_pool_destroy", "mlora_pool_load_slot",
            "mlora_build_segments", "mlora_status_string",
            "mlora_version", "mlora_pool_slot_generation", "mlora_slot_cache_create",
            "mlora_slot_cache_destroy", "mlora_slot_cache_acquire", "mlora_slot_cache_release",
+           "mlora_mx_scale_bytes", "mlora_mx_quantize", "mlora_mx_dequantize", "mlora_mx_gemm_apply",
+           "mlora_group_rows", "mlora_gather_rows", "mlora_combine_rows", "mlora_combine_rows_backward",
            "mlora_slot_cache_invalidate", "mlora_slot_cache_lookup", "mlora_slot_cache_stats")
 
 
@@ -52,6 +54,16 @@ class SegmentsStruct(ctypes.Structure):
                 ("token_indices", ctypes.c_void_p), ("generations", ctypes.c_void_p)]
 
 
+class MxStruct(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("n_cols", ctypes.c_int32), ("ld", ctypes.c_int64),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class RowGroupsStruct(ctypes.Structure):
+    _fields_ = [("offsets", ctypes.c_void_p), ("slots", ctypes.c_void_p), ("ranks", ctypes.c_void_p),
+                ("order", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m segmented_rank_gemm_02_b200.build`")
@@ -59,6 +71,7 @@ def _load():
     vp, i32, i64, f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
     i32p = ctypes.POINTER(ctypes.c_int32)
     seg_p = ctypes.POINTER(SegmentsStruct)
+    mx_p = ctypes.POINTER(MxStruct)
     sig = {
         "mlora_pool_create": [i32, i32, i32, i32, ctypes.POINTER(vp)],
         "mlora_pool_destroy": [vp],
@@ -75,6 +88,13 @@ def _load():
         "mlora_base_gemm_apply": [vp, seg_p, vp, i64, vp, i64, vp, i64, vp],
         "mlora_apply_multi": [ctypes.POINTER(vp), i32, seg_p, vp, i64, ctypes.POINTER(vp),
                               ctypes.POINTER(i64), vp],
+        "mlora_mx_quantize": [vp, i32, i64, mx_p, vp],
+        "mlora_mx_dequantize": [mx_p, vp, i32, i64, vp],
+        "mlora_mx_gemm_apply": [vp, seg_p, vp, i64, mx_p, mx_p, vp, i32, i64, vp],
+        "mlora_group_rows": [vp, vp, i32, i32, ctypes.POINTER(RowGroupsStruct), vp],
+        "mlora_gather_rows": [vp, vp, i32, i32, vp, i64, i32, i32, i32, vp, i64, vp],
+        "mlora_combine_rows": [vp, vp, vp, i32, i32, vp, i64, i32, i32, i32, vp, i64, vp],
+        "mlora_combine_rows_backward": [vp, vp, vp, i32, i32, vp, i64, vp, i64, i32, i32, i32, vp, i64, vp, vp],
         "mlora_build_segments": [vp, i32, vp, vp, vp, i32p, i32p, vp, vp],
         "mlora_pool_slot_generation": [vp, i32, ctypes.POINTER(ctypes.c_uint32)],
         "mlora_slot_cache_create": [i32, ctypes.POINTER(vp)],
@@ -91,6 +111,8 @@ def _load():
         fn.restype = ctypes.c_int
     lib.mlora_status_string.argtypes = [ctypes.c_int]
     lib.mlora_status_string.restype = ctypes.c_char_p
+    lib.mlora_mx_scale_bytes.argtypes = [i32, i32]
+    lib.mlora_mx_scale_bytes.restype = i64
     lib.mlora_version.argtypes = []
     lib.mlora_version.restype = ctypes.c_int32
     return lib
@@ -343,6 +365,217 @@ def expand(pool: Pool, segs: DeviceSegments, H, Y, stream=None) -> None:
     """Y[t_p] = bf16(Y[t_p] + s H[p, :r] B^T) in place (mlora_expand)."""
     _check(lib().mlora_expand(pool.handle, ctypes.byref(segs.struct), _ptr(H), _ld(H, "H"),
                              _ptr(Y), _ld(Y, "Y"), _stream_ptr(stream)), "mlora_expand")
+
+
+class MxMatrix:
+    """A 4-bit microscaled matrix (mlora_mx_matrix): packed codes [n_rows, 16 per block of 32
+    columns] and scale tiles [ceil(n_rows / 128), 2 ceil(n_cols / 256), 32, 4, 4], uint8, allocated
+    on `device` or given (a checkpoint's own, already in this layout)."""
+
+    def __init__(self, n_rows: int, n_cols: int, device=None, codes=None, scales=None):
+        import torch
+        n_rows, n_cols = int(n_rows), int(n_cols)
+        if n_rows < 0 or n_cols <= 0 or n_cols % 8 != 0:
+            raise ValueError("a 4-bit matrix has n_rows >= 0 and n_cols a positive multiple of 8")
+        row_bytes = (n_cols + 31) // 32 * 16
+        shape = ((n_rows + 127) // 128, 2 * ((n_cols + 255) // 256), 32, 4, 4)
+        if codes is None:
+            codes = torch.empty((n_rows, row_bytes), dtype=torch.uint8, device=device)
+        if scales is None:
+            scales = torch.empty(shape, dtype=torch.uint8, device=codes.device)
+        if codes.dtype != torch.uint8 or tuple(codes.shape) != (n_rows, row_bytes):
+            raise ValueError(f"codes must be uint8 [{n_rows}, {row_bytes}]")
+        if scales.dtype != torch.uint8 or tuple(scales.shape) != shape or not scales.is_contiguous():
+            raise ValueError(f"scales must be contiguous uint8 {list(shape)}")
+        if scales.device != codes.device:
+            raise ValueError("codes and scales must be on one device")
+        self.codes, self.scales = codes, scales
+        self.n_rows, self.n_cols = n_rows, n_cols
+        self.struct = MxStruct(n_rows, n_cols, _ld(codes, "codes") if n_rows > 1 else row_bytes, _ptr(codes),
+                               _ptr(scales))
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def _on_device(t, what: str):
+    """The device of a CUDA tensor, made current for the call (its stream is that device's)."""
+    import torch
+    if not t.is_cuda:
+        raise ValueError(f"{what} must be on a CUDA device")
+    return torch.cuda.device(t.device)
+
+
+def _float_code(t, what: str) -> int:
+    code = _dtype_code(t)
+    if code == DTYPE_FP8_E4M3:
+        raise ValueError(f"{what} must be bf16, fp16 or fp32")
+    return code
+
+
+def mx_quantize(X, out: Optional[MxMatrix] = None, stream=None) -> MxMatrix:
+    """X [n, d] (bf16, fp16 or fp32, on the GPU) as a 4-bit microscaled matrix (mlora_mx_quantize)."""
+    code = _float_code(X, "X")
+    ld = _ld(X, "X")
+    n, d = X.shape
+    with _on_device(X, "X"):
+        if out is None:
+            out = MxMatrix(n, d, X.device)
+        elif (out.n_rows, out.n_cols, out.device) != (n, d, X.device):
+            raise ValueError("out must have X's shape and device")
+        _check(lib().mlora_mx_quantize(_ptr(X), code, ld, ctypes.byref(out.struct), _stream_ptr(stream)),
+               "mlora_mx_quantize")
+    return out
+
+
+def mx_dequantize(Q: MxMatrix, out=None, dtype=None, stream=None):
+    """The values Q stands for, in `dtype` (bf16 unless given) or into `out` (mlora_mx_dequantize)."""
+    import torch
+    with _on_device(Q.codes, "Q"):
+        if out is None:
+            out = torch.empty((Q.n_rows, Q.n_cols), dtype=dtype or torch.bfloat16, device=Q.device)
+        elif tuple(out.shape) != (Q.n_rows, Q.n_cols) or out.device != Q.device or dtype not in (None, out.dtype):
+            raise ValueError("out must have Q's shape and device, and dtype if both are given")
+        _check(lib().mlora_mx_dequantize(ctypes.byref(Q.struct), _ptr(out), _float_code(out, "out"), _ld(out, "out"),
+                                         _stream_ptr(stream)), "mlora_mx_dequantize")
+    return out
+
+
+def mx_gemm_apply(pool: Pool, segs: Optional["DeviceSegments"], X, Xq: MxMatrix, W: MxMatrix, Y, stream=None) -> None:
+    """Y = round(Xq W^T + s (X A^T) B^T) for adapter rows, round(Xq W^T) for the others, in one pass
+    (mlora_mx_gemm_apply).  Xq [n_rows, d_in] and W [d_out, d_in] 4-bit, X the bf16 activations that
+    Xq was quantised from (not read, and may be None, if segs is None), Y bf16, fp16 or fp32."""
+    if tuple(Y.shape) != (Xq.n_rows, pool.d_out):
+        raise ValueError("Y must be [rows of Xq, d_out]")
+    if segs is not None and (X is None or tuple(X.shape) != (Xq.n_rows, pool.d_in) or _dtype_code(X) != DTYPE_BF16):
+        raise ValueError("X must be bf16 [rows of Xq, d_in]")
+    if not (Xq.device == W.device == Y.device and (X is None or X.device == Y.device)):
+        raise ValueError("X, Xq, W and Y must be on one device")
+    with _on_device(Y, "Y"):
+        _check(lib().mlora_mx_gemm_apply(pool.handle, ctypes.byref(segs.struct) if segs is not None else None,
+                                         _ptr(X), _ld(X, "X") if X is not None else 0, ctypes.byref(Xq.struct),
+                                         ctypes.byref(W.struct), _ptr(Y), _float_code(Y, "Y"), _ld(Y, "Y"),
+                                         _stream_ptr(stream)), "mlora_mx_gemm_apply")
+
+
+class RowGroups:
+    """Rows grouped by slot on the device (mlora_group_rows), usable as DeviceSegments: of the
+    batch's own rows with one slot per row, of the rows in grouped order (gather_rows) with more.
+
+    offsets, slots, ranks, order, positions: int32 device tensors (see mlora.h)."""
+
+    def __init__(self, pool: Pool, n_rows: int, top_k: int, device, max_segment_rows: int = 0):
+        import torch
+        n = n_rows * top_k
+        S = min(pool.n_slots + 1, n)
+        buf = torch.empty(3 * S + 1 + 2 * n, dtype=torch.int32, device=device)
+        self.offsets, self.slots, self.ranks, self.order, self.positions = torch.split(buf, [S + 1, S, S, n, n])
+        self.pool, self.n_rows, self.top_k = pool, n_rows, top_k
+        at = buf.data_ptr()
+        self._out = RowGroupsStruct(at, at + 4 * (S + 1), at + 4 * (2 * S + 1), at + 4 * (3 * S + 1),
+                                    at + 4 * (3 * S + 1 + n))
+        self.struct = SegmentsStruct(S, n, n, int(max_segment_rows), self._out.offsets, self._out.slots,
+                                     self._out.ranks, None, self._out.order if top_k == 1 else None, None)
+
+    @property
+    def n_tokens(self) -> int:
+        return self.n_rows * self.top_k
+
+
+def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segment_rows: int = 0,
+               stream=None) -> RowGroups:
+    """Sort rows by adapter slot on the device (mlora_group_rows).  row_slots: int32 [n_rows] or
+    [n_rows, top_k], contiguous, -1 = base model.  `out` reuses a RowGroups of the same sizes (a
+    captured graph's).  max_segment_rows: the hint of mlora_segments, if the caller knows one."""
+    import torch
+    if row_slots.dtype != torch.int32 or row_slots.dim() not in (1, 2) or not row_slots.is_contiguous():
+        raise ValueError("row_slots must be contiguous int32 [n_rows] or [n_rows, top_k]")
+    n_rows = row_slots.shape[0]
+    top_k = 1 if row_slots.dim() == 1 else row_slots.shape[1]
+    if top_k < 1:
+        raise ValueError("row_slots needs at least one slot per row")
+    with _on_device(row_slots, "row_slots"):
+        if out is None:
+            out = RowGroups(pool, n_rows, top_k, row_slots.device, max_segment_rows)
+        elif (out.pool is not pool or (out.n_rows, out.top_k) != (n_rows, top_k)
+              or out.offsets.device != row_slots.device):
+            raise ValueError("out must be of this pool, the same sizes and device")
+        _check(lib().mlora_group_rows(pool.handle, _ptr(row_slots), n_rows, top_k, ctypes.byref(out._out),
+                                      _stream_ptr(stream)), "mlora_group_rows")
+    return out
+
+
+def _rows_of(t, n: int, like, what: str):
+    if t.dim() != 2 or t.shape[0] != n or (like is not None and (t.shape[1], t.dtype, t.device) != (
+            like.shape[1], like.dtype, like.device)):
+        raise ValueError(f"{what} has the wrong shape, dtype or device")
+    return _ld(t, what) if n > 1 else max(int(t.stride(0)), int(t.shape[1]))
+
+
+def _weights_ptr(groups: RowGroups, w, device, what: str):
+    import torch
+    if w is None:
+        return None
+    if w.dtype != torch.float32 or w.numel() != groups.n_tokens or not w.is_contiguous() or w.device != device:
+        raise ValueError(f"{what} must be contiguous fp32 [n_rows, top_k] on the rows' device")
+    return _ptr(w)
+
+
+def gather_rows(groups: RowGroups, X, Xs=None, stream=None):
+    """Xs[positions[t, j]] = X[t]: the rows in grouped order (mlora_gather_rows).  The gradient of X
+    is combine_rows(groups, dXs)."""
+    import torch
+    code = _float_code(X, "X")
+    ldx = _rows_of(X, groups.n_rows, None, "X")
+    with _on_device(X, "X"):
+        if Xs is None:
+            Xs = torch.empty((groups.n_tokens, X.shape[1]), dtype=X.dtype, device=X.device)
+        ldxs = _rows_of(Xs, groups.n_tokens, X, "Xs")
+        _check(lib().mlora_gather_rows(groups.pool.handle, _ptr(groups.positions), groups.n_rows, groups.top_k, _ptr(X),
+                                       ldx, code, X.shape[1], groups.n_tokens, _ptr(Xs), ldxs, _stream_ptr(stream)),
+               "mlora_gather_rows")
+    return Xs
+
+
+def combine_rows(groups: RowGroups, Ys, weights=None, Y=None, stream=None):
+    """Y[t] = sum_j weights[t, j] Ys[positions[t, j]] (mlora_combine_rows); weights fp32 or None (ones)."""
+    import torch
+    code = _float_code(Ys, "Ys")
+    ldys = _rows_of(Ys, groups.n_tokens, None, "Ys")
+    w = _weights_ptr(groups, weights, Ys.device, "weights")
+    with _on_device(Ys, "Ys"):
+        if Y is None:
+            Y = torch.empty((groups.n_rows, Ys.shape[1]), dtype=Ys.dtype, device=Ys.device)
+        ldy = _rows_of(Y, groups.n_rows, Ys, "Y")
+        _check(lib().mlora_combine_rows(groups.pool.handle, _ptr(groups.positions), w, groups.n_rows, groups.top_k,
+                                        _ptr(Ys), ldys, code, Ys.shape[1], groups.n_tokens, _ptr(Y), ldy,
+                                        _stream_ptr(stream)), "mlora_combine_rows")
+    return Y
+
+
+def combine_rows_backward(groups: RowGroups, dY, Ys, weights=None, dYs=None, dweights=None, stream=None):
+    """(dYs, dweights) of combine_rows from dY (mlora_combine_rows_backward).  Without weights only dYs
+    is computed (dweights is None, Ys may be None) unless a dweights tensor is given."""
+    import torch
+    code = _float_code(dY, "dY")
+    lddy = _rows_of(dY, groups.n_rows, None, "dY")
+    w = _weights_ptr(groups, weights, dY.device, "weights")
+    with _on_device(dY, "dY"):
+        if dYs is None:
+            dYs = torch.empty((groups.n_tokens, dY.shape[1]), dtype=dY.dtype, device=dY.device)
+        lddys = _rows_of(dYs, groups.n_tokens, dY, "dYs")
+        if dweights is None and weights is not None:
+            dweights = torch.empty((groups.n_rows, groups.top_k), dtype=torch.float32, device=dY.device)
+        dw = _weights_ptr(groups, dweights, dY.device, "dweights")
+        if dw is not None and Ys is None:
+            raise ValueError("the gradient of the weights needs Ys")
+        ldys = _rows_of(Ys, groups.n_tokens, dY, "Ys") if Ys is not None else 0
+        _check(lib().mlora_combine_rows_backward(groups.pool.handle, _ptr(groups.positions), w, groups.n_rows,
+                                                 groups.top_k, _ptr(dY), lddy, _ptr(Ys), ldys, code, dY.shape[1],
+                                                 groups.n_tokens, _ptr(dYs), lddys, dw, _stream_ptr(stream)),
+               "mlora_combine_rows_backward")
+    return dYs, dweights
 
 
 class SlotCache:

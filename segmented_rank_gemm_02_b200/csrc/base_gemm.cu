@@ -43,6 +43,7 @@
 
 #include "kernels.cuh"
 #include "ptx.cuh"
+#include "slot_operand.cuh"
 
 namespace mlora {
 
@@ -136,8 +137,6 @@ __device__ __forceinline__ void tile_coords(const GemmParams &p, int t, int &mb,
 // Cluster address of `bar` in the even CTA of the pair (rank 0 of the cluster).
 __device__ __forceinline__ uint32_t leader_bar(const uint64_t *bar) { return map_to_rank(smem_addr(bar), 0); }
 
-__device__ __forceinline__ int bucket_index(int R) { return R <= 8 ? 0 : R <= 16 ? 1 : R <= 32 ? 2 : 3; }
-
 }  // namespace
 
 // ------------------------------------------------------------------ row map
@@ -197,8 +196,9 @@ __global__ void __launch_bounds__(256) row_map_kernel(const __grid_constant__ Ti
     }
 }
 
-// One CTA of 256 threads per 256-row block: the distinct slots of the block's rows in
+// One CTA of PM threads per PM-row block (PM = 128 or 256): the distinct slots of the block's rows in
 // order of first appearance, as out[0] = count, then (slot, rank bucket) pairs.
+template <int PM>
 __global__ void __launch_bounds__(PM) block_slots_kernel(const int4 *row_info, int n_rows, int32_t *out)
 {
     __shared__ int s_slot[PM];
@@ -234,45 +234,6 @@ __global__ void __launch_bounds__(PM) block_slots_kernel(const int4 *row_info, i
         o[2 + 2 * idx] = rank_bucket(rank);
     }
     if (tid == 0) o[0] = total;
-}
-
-// One row of the LoRA operand: s * H[row, 0:rank) (zeros past rank, all zeros for
-// rank 0) as bf16 hi + lo parts in the K-major no-swizzle layout [RK/8][16][8][8].
-// The row's loads are all issued before any is used.
-template <int RK>
-__device__ __forceinline__ void stage_operand(uint8_t *hi, uint8_t *lo, const float *hsrc, int rank, float sc, int r)
-{
-    float h[RK];
-    if (rank == RK) {
-#pragma unroll
-        for (int i = 0; i < RK / 4; ++i) {
-            const float4 v = reinterpret_cast<const float4 *>(hsrc)[i];
-            h[4 * i] = v.x;
-            h[4 * i + 1] = v.y;
-            h[4 * i + 2] = v.z;
-            h[4 * i + 3] = v.w;
-        }
-    } else {
-#pragma unroll
-        for (int c = 0; c < RK; ++c) h[c] = c < rank ? hsrc[c] : 0.f;
-    }
-#pragma unroll
-    for (int cg = 0; cg < RK / 8; ++cg) {
-        uint4 vh, vl;
-        uint32_t *ph = reinterpret_cast<uint32_t *>(&vh);
-        uint32_t *pl = reinterpret_cast<uint32_t *>(&vl);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float h0, l0, h1, l1;
-            split_bf16(sc * h[8 * cg + 2 * c], h0, l0);
-            split_bf16(sc * h[8 * cg + 2 * c + 1], h1, l1);
-            ph[c] = pack_bf16x2(h0, h1);
-            pl[c] = pack_bf16x2(l0, l1);
-        }
-        const int off = (cg * (GM / 8) + r / 8) * 128 + (r % 8) * 16;
-        *reinterpret_cast<uint4 *>(hi + off) = vh;
-        *reinterpret_cast<uint4 *>(lo + off) = vl;
-    }
 }
 
 // ------------------------------------------------------------------ GEMM
@@ -599,11 +560,13 @@ cudaError_t launch_row_map(const TileParams &p, int4 *row_info, cudaStream_t str
     return cudaGetLastError();
 }
 
-cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream)
+cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream,
+                               int block_rows)
 {
-    const int n_mblk = (n_rows + PM - 1) / PM;
+    const int n_mblk = (n_rows + block_rows - 1) / block_rows;
     if (n_mblk <= 0) return cudaSuccess;
-    block_slots_kernel<<<n_mblk, PM, 0, stream>>>(row_info, n_rows, block_slots);
+    if (block_rows == 128) block_slots_kernel<128><<<n_mblk, 128, 0, stream>>>(row_info, n_rows, block_slots);
+    else block_slots_kernel<PM><<<n_mblk, PM, 0, stream>>>(row_info, n_rows, block_slots);
     return cudaGetLastError();
 }
 

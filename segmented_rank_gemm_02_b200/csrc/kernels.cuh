@@ -206,8 +206,9 @@ struct GemmParams {
 // row_info for every row (memset to -1, then the valid segments' rows); reports the
 // segments' problems in p.status.
 cudaError_t launch_row_map(const TileParams &p, int4 *row_info, cudaStream_t stream);
-// The distinct slots of each 256-row block of rows.
-cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream);
+// The distinct slots of each block of `block_rows` rows (256 or 128).
+cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream,
+                               int block_rows = kGemmRows);
 // Tile width (256 or 512 columns of Y) for n_mblk 256-row blocks and d_out columns.
 int choose_gemm_cols(int n_mblk, int d_out);
 // Persistent GEMM over all (256-row, gn-column) tiles, one pair of CTAs per two SMs;
@@ -215,5 +216,33 @@ int choose_gemm_cols(int n_mblk, int d_out);
 // launch after the kernel before it, whose results (H) it reads only after waiting.
 cudaError_t launch_base_gemm(int gn, const GemmParams &p, cudaStream_t stream, bool pdl);
 cudaError_t prepare_base_gemm();
+
+// ---- 4-bit base GEMM + LoRA (mx_gemm.cu)
+
+constexpr int kMxTileRows = 128;   // rows of Y per tile (and per block of slot lists)
+
+// Everything one launch of the 4-bit GEMM needs.  Passed by value.
+struct MxGemmParams {
+    CUtensorMap x_map, w_map;   // codes as bytes [rows][row bytes], box 128 x 128, 128-byte swizzle
+    CUtensorMap b_map[4];       // the pool's B blocks, as in GemmParams
+    int32_t b_col_div;
+    const uint8_t *x_scales, *w_scales;   // scale tiles, 1 KB per 128 rows and 256 columns
+    const int4 *row_info;       // as in GemmParams; unused without LoRA
+    const int32_t *block_slots; // [n_mblk][kBlockSlotsPitch], blocks of kMxTileRows rows
+    const float *H;
+    int64_t ldh;
+    void *Y;                    // [n_rows][ldy], written for every row
+    int64_t ldy;
+    int32_t y_type;             // 0 bf16, 1 fp16, 2 fp32
+    unsigned int *status;
+    int32_t n_rows, d_in, d_out, n_mblk, n_nblk;
+};
+
+// Y = X W^T (+ the slots' low-rank products if rank_bucket_max > 0, the pool's largest bucket).
+cudaError_t launch_mx_gemm(const MxGemmParams &p, int rank_bucket_max, cudaStream_t stream);
+cudaError_t prepare_mx_gemm();
+
+// ---- rows grouped by slot (rows.cu)
+cudaError_t prepare_row_kernels();
 
 }  // namespace mlora

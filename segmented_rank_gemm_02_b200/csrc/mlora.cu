@@ -54,24 +54,7 @@ namespace {
 
 using mlora::rank_bucket;
 
-// Runs the body with the pool's device current, restoring the caller's device.
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev)
-    {
-        if (cudaGetDevice(&prev) != cudaSuccess) {
-            ok = false;
-            return;
-        }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard()
-    {
-        int cur = -1;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
+using DeviceGuard = mlora_device_guard;   // runs the body with the pool's device current
 
 std::mutex g_prep_mutex;
 bool g_prepared[128] = {};
@@ -84,6 +67,8 @@ mlora_status prepare_device(int dev)
     if (mlora::prepare_tile_kernels() != cudaSuccess) return MLORA_ERR_CUDA;
     if (mlora::prepare_long_kernels() != cudaSuccess) return MLORA_ERR_CUDA;
     if (mlora::prepare_base_gemm() != cudaSuccess) return MLORA_ERR_CUDA;
+    if (mlora::prepare_mx_gemm() != cudaSuccess) return MLORA_ERR_CUDA;
+    if (mlora::prepare_row_kernels() != cudaSuccess) return MLORA_ERR_CUDA;
     g_prepared[dev] = true;
     return MLORA_OK;
 }
@@ -171,6 +156,21 @@ bool encode_rows_map(CUtensorMap *map, const void *base, int64_t rows, int64_t c
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, elem,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Rows of packed 4-bit codes as bytes [rows, cols] with row stride ld (bytes), 128-byte
+// swizzle, box 128 bytes x 128 rows; what lies outside reads as zero codes.
+bool encode_codes_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr || base == nullptr || rows <= 0 || cols <= 0) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)ld};
+    cuuint32_t box[2] = {128, 128};
+    cuuint32_t elem[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, elem,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // The pool's B blocks as a 4-D tensor [slot][rank group][d_out][8] (bf16), box
@@ -374,6 +374,15 @@ mlora_status mlora_apply_with_workspace(mlora_pool *pool, const mlora_segments *
 }
 
 int mlora_pool_device(const mlora_pool *pool) { return pool ? pool->device : -1; }
+
+bool mlora_pool_get_view(const mlora_pool *pool, mlora_pool_view *view)
+{
+    if (pool == nullptr) return false;
+    *view = mlora_pool_view{pool->device, pool->n_slots, pool->d_rank, pool->d_status};
+    return true;
+}
+
+mlora_status mlora_prepare_device(int dev) { return prepare_device(dev); }
 
 extern "C" {
 
@@ -731,6 +740,80 @@ mlora_status mlora_base_gemm_apply(mlora_pool *pool, const mlora_segments *segs,
     g.n_mblk = (int32_t)n_mblk;
     g.n_nblk = (int32_t)n_nblk;
     return mlora::launch_base_gemm(gn, g, cs, pdl) == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
+}
+
+mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, const void *X, int64_t ldx,
+                                 const mlora_mx_matrix *Xq, const mlora_mx_matrix *W, void *Y, int32_t y_dtype,
+                                 int64_t ldy, void *stream)
+{
+    if (pool == nullptr || Xq == nullptr || W == nullptr) return MLORA_ERR_INVALID_ARG;
+    mlora_status st = mlora_mx_check_matrix(Xq);
+    if (st == MLORA_OK) st = mlora_mx_check_matrix(W);
+    if (st == MLORA_OK && segs != nullptr) st = check_segments(pool, segs);
+    if (st != MLORA_OK) return st;
+    if (Xq->n_cols != pool->d_in || W->n_cols != pool->d_in || W->n_rows != pool->d_out) return MLORA_ERR_INVALID_ARG;
+    if (segs != nullptr && segs->n_rows != Xq->n_rows) return MLORA_ERR_INVALID_ARG;
+    if (y_dtype != MLORA_DTYPE_BF16 && y_dtype != MLORA_DTYPE_FP16 && y_dtype != MLORA_DTYPE_FP32)
+        return MLORA_ERR_INVALID_ARG;
+    if (Xq->n_rows == 0) return MLORA_OK;
+    const bool lora = segs != nullptr && segs->n_segments > 0 && segs->n_tokens > 0;
+    if (Y == nullptr || !aligned16(Y) || ldy < pool->d_out || ldy % (y_dtype == MLORA_DTYPE_FP32 ? 4 : 8) != 0)
+        return MLORA_ERR_INVALID_ARG;
+    if (lora && (X == nullptr || !aligned16(X) || ldx < pool->d_in || ldx % 8 != 0)) return MLORA_ERR_INVALID_ARG;
+    if (!pool->b_maps_ok) return MLORA_ERR_UNSUPPORTED;
+    DeviceGuard guard(pool->device);
+    if (!guard.ok) return MLORA_ERR_CUDA;
+    st = prepare_device(pool->device);
+    if (st != MLORA_OK) return st;
+    cudaStream_t cs = static_cast<cudaStream_t>(stream);
+
+    mlora::MxGemmParams g{};
+    const int64_t row_bytes = round_up(pool->d_in, 32) / 2;
+    if (!encode_codes_map(&g.x_map, Xq->codes, Xq->n_rows, row_bytes, Xq->ld) ||
+        !encode_codes_map(&g.w_map, W->codes, W->n_rows, row_bytes, W->ld))
+        return MLORA_ERR_CUDA;
+    g.x_scales = static_cast<const uint8_t *>(Xq->scales);
+    g.w_scales = static_cast<const uint8_t *>(W->scales);
+    g.Y = Y;
+    g.ldy = ldy;
+    g.y_type = y_dtype;
+    g.status = pool->d_status;
+    g.n_rows = Xq->n_rows;
+    g.d_in = pool->d_in;
+    g.d_out = pool->d_out;
+    g.n_mblk = (Xq->n_rows + mlora::kMxTileRows - 1) / mlora::kMxTileRows;
+    g.n_nblk = (pool->d_out + 127) / 128;
+    if (!lora) return mlora::launch_mx_gemm(g, 0, cs) == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
+
+    // workspace: H (grouped order), the row map, the slot lists of the row blocks
+    const int rk = std::max(16, pool->r_bucket_max);
+    const size_t h_bytes = (size_t)round_up((int64_t)segs->n_tokens * rk * 4, 256);
+    const size_t map_bytes = (size_t)round_up((int64_t)segs->n_rows * 16, 256);
+    const size_t slot_bytes = (size_t)g.n_mblk * mlora::kBlockSlotsPitch * 4;
+    std::lock_guard<std::mutex> lock(pool->ws_mutex);   // held until the kernels are launched
+    st = ensure_workspace(pool, h_bytes + map_bytes + slot_bytes, cs);
+    if (st != MLORA_OK) return st;
+    uint8_t *ws = reinterpret_cast<uint8_t *>(pool->ws);
+    float *H = reinterpret_cast<float *>(ws);
+    int4 *row_info = reinterpret_cast<int4 *>(ws + h_bytes);
+    int32_t *block_slots = reinterpret_cast<int32_t *>(ws + h_bytes + map_bytes);
+    mlora::TileParams p = base_params(pool, segs);
+    p.X = static_cast<const __nv_bfloat16 *>(X);
+    p.ldx = ldx;
+    p.H = H;
+    p.ldh = rk;
+    if (mlora::launch_row_map(p, row_info, cs) != cudaSuccess ||
+        mlora::launch_block_slots(row_info, segs->n_rows, block_slots, cs, mlora::kMxTileRows) != cudaSuccess)
+        return MLORA_ERR_CUDA;
+    st = launch(pool, segs, mlora::MODE_SHRINK, p, stream);
+    if (st != MLORA_OK) return st;
+    for (int i = 0; i < 4; ++i) g.b_map[i] = pool->b_maps_wide_ok ? pool->b_maps_wide[i] : pool->b_maps[i];
+    g.b_col_div = pool->b_maps_wide_ok ? 32 : 1;
+    g.row_info = row_info;
+    g.block_slots = block_slots;
+    g.H = H;
+    g.ldh = rk;
+    return mlora::launch_mx_gemm(g, pool->r_bucket_max, cs) == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
 }
 
 mlora_status mlora_apply_multi(mlora_pool *const *pools, int32_t n_proj, const mlora_segments *segs,

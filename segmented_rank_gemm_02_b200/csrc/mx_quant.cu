@@ -1,0 +1,297 @@
+// mx_quant.cu -- rows to 4-bit microscaled floating point and back.
+//
+// Format (OCP microscaling formats, MXFP4): a block of 32 consecutive elements of a row has
+// the scale 2^e, e = floor(log2(max |x|)) - 2 clamped to [-127, 127], kept as the byte
+// e + 127; each element is x / 2^e rounded to the nearest e2m1 value (0, .5, 1, 1.5, 2, 3, 4,
+// 6 with a sign; ties to the even code, beyond 6 to 6).  The byte is the fp32 exponent field of
+// the block's maximum less two (not below zero), and x / 2^e is an exact product, so the
+// conversion's rounding is the only one.  A block that holds an infinity or a NaN gets the scale
+// byte 255 (NaN) and zero codes: all its values read back as NaN.
+//
+// Layout: two codes per byte, the first in the low half, rows padded with zero codes to whole
+// blocks; scale bytes in tiles of 128 rows x 4 blocks (512 bytes) as the tensor core wants them
+// in tensor memory: row r of the tile and block b at 16 (r % 32) + 4 (r / 32) + b.  A warp
+// takes 256 columns of rows r, r + 32, r + 64, r + 96 of a tile: eight elements per lane and
+// row, all loads issued before the first is used, and the 4 x 4 scale bytes of one r stored as
+// one 16-byte vector.  HBM bound: n d (size + 17/32) bytes.
+#include "mlora.h"
+
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_fp16.h>
+
+#include "internal.h"
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace mlora {
+
+namespace {
+
+constexpr int kQuantThreads = 256;
+constexpr int kTileRowsMx = 128;
+
+// Eight elements of type T at `p` as fp32.
+template <typename T>
+struct Eight;
+template <>
+struct Eight<__nv_bfloat16> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    }
+    static __device__ __forceinline__ void store(__nv_bfloat16 *p, const float (&f)[8])
+    {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
+                                                   pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    }
+};
+template <>
+struct Eight<__half> {
+    uint4 v;
+    __device__ __forceinline__ void load(const __half *p) { v = __ldg(reinterpret_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void zero() { v = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 two = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+            f[2 * i] = two.x;
+            f[2 * i + 1] = two.y;
+        }
+    }
+    static __device__ __forceinline__ void store(__half *p, const float (&f)[8])
+    {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+};
+template <>
+struct Eight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p)
+    {
+        a = __ldg(reinterpret_cast<const float4 *>(p));
+        b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+    __device__ __forceinline__ void get(float (&f)[8]) const
+    {
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+    }
+    static __device__ __forceinline__ void store(float *p, const float (&f)[8])
+    {
+        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+};
+
+struct MxRows {
+    uint8_t *codes;
+    int64_t ld;        // bytes
+    uint8_t *scales;
+    int32_t n_rows, n_cols;
+    int32_t chunks;    // 256-column chunks of a row
+};
+
+// Warp -> (128-row tile, r of 0..31, 256-column chunk).
+__device__ __forceinline__ bool my_unit(const MxRows &q, int64_t w, int &row0, int &chunk)
+{
+    const int64_t tiles = (q.n_rows + kTileRowsMx - 1) / kTileRowsMx;
+    if (w >= tiles * 32 * q.chunks) return false;
+    chunk = (int)(w % q.chunks);
+    const int64_t r = w / q.chunks;
+    row0 = (int)(r / 32 * kTileRowsMx + r % 32);
+    return true;
+}
+
+// The 16 scale bytes of (row0's r, tile `half` of the chunk).
+__device__ __forceinline__ uint8_t *scale_vec(const MxRows &q, int row0, int chunk, int half)
+{
+    return q.scales + ((int64_t)(row0 / kTileRowsMx) * 2 * q.chunks + 2 * chunk + half) * 512 + (row0 % 32) * 16;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads) mx_quantize_kernel(const T *X, int64_t ldx, const MxRows q)
+{
+    const int lane = threadIdx.x & 31;
+    int row0, chunk;
+    if (!my_unit(q, ((int64_t)blockIdx.x * kQuantThreads + threadIdx.x) >> 5, row0, chunk)) return;
+    const int col = chunk * 256 + lane * 8;
+    Eight<T> x[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int row = row0 + 32 * u;
+        if (row < q.n_rows && col < q.n_cols) x[u].load(X + row * ldx + col);
+        else x[u].zero();
+    }
+    uint32_t words[4];   // per row: the scale bytes of this half's four blocks
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        float f[8];
+        x[u].get(f);
+        uint32_t big = 0;   // largest magnitude, as bits: NaN above infinity above the rest
+#pragma unroll
+        for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(f[i]) & 0x7fffffffu);
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const bool finite = big < 0x7f800000u;
+        const int field = (int)(big >> 23);
+        const uint32_t s = finite ? (uint32_t)max(field - 2, 0) : 255u;
+        // 2^-e; a block that is not finite gets zero codes
+        const float inv = finite ? __uint_as_float((254u - s) << 23) : 0.f;
+        uint32_t c = 0;
+        if (finite) {
+            c = e2m1x8(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv, f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
+        }
+        const int row = row0 + 32 * u;
+        if (row < q.n_rows && col < (q.n_cols + 31) / 32 * 32)
+            *reinterpret_cast<uint32_t *>(q.codes + row * q.ld + col / 2) = c;
+        uint32_t w = s << (8 * ((lane >> 2) & 3));
+        w |= __shfl_xor_sync(0xffffffffu, w, 4);
+        w |= __shfl_xor_sync(0xffffffffu, w, 8);
+        words[u] = w;
+    }
+    if ((lane & 15) == 0)
+        *reinterpret_cast<uint4 *>(scale_vec(q, row0, chunk, lane >> 4)) =
+            make_uint4(words[0], words[1], words[2], words[3]);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kQuantThreads) mx_dequantize_kernel(const MxRows q, T *X, int64_t ldx)
+{
+    const int lane = threadIdx.x & 31;
+    int row0, chunk;
+    if (!my_unit(q, ((int64_t)blockIdx.x * kQuantThreads + threadIdx.x) >> 5, row0, chunk)) return;
+    const int col = chunk * 256 + lane * 8;
+    const uint4 sv = *reinterpret_cast<const uint4 *>(scale_vec(q, row0, chunk, lane >> 4));
+    const uint32_t words[4] = {sv.x, sv.y, sv.z, sv.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int row = row0 + 32 * u;
+        c[u] = row < q.n_rows && col < q.n_cols ? *reinterpret_cast<const uint32_t *>(q.codes + row * q.ld + col / 2) : 0u;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int row = row0 + 32 * u;
+        if (row >= q.n_rows || col >= q.n_cols) continue;
+        const uint32_t s = (words[u] >> (8 * ((lane >> 2) & 3))) & 0xffu;
+        // 2^(s - 127): subnormal for s = 0, NaN for 255
+        const float scale = __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
+        float f[8];
+        e2m1x8_to_float(c[u], f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] *= scale;
+        Eight<T>::store(X + row * ldx + col, f);
+    }
+}
+
+unsigned quant_blocks(const MxRows &q)
+{
+    const int64_t warps = ((int64_t)q.n_rows + kTileRowsMx - 1) / kTileRowsMx * 32 * q.chunks;
+    return (unsigned)((warps * 32 + kQuantThreads - 1) / kQuantThreads);
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+mlora_status check_operand(const void *X, int32_t dtype, int64_t ldx, const mlora_mx_matrix *Q, bool &empty)
+{
+    if (Q == nullptr) return MLORA_ERR_INVALID_ARG;
+    if (dtype != MLORA_DTYPE_BF16 && dtype != MLORA_DTYPE_FP16 && dtype != MLORA_DTYPE_FP32) return MLORA_ERR_INVALID_ARG;
+    mlora_status st = mlora_mx_check_matrix(Q);
+    if (st != MLORA_OK) return st;
+    empty = Q->n_rows == 0;
+    if (empty) return MLORA_OK;
+    if (X == nullptr || !aligned16(X) || ldx < Q->n_cols || ldx % (dtype == MLORA_DTYPE_FP32 ? 4 : 8) != 0)
+        return MLORA_ERR_INVALID_ARG;
+    return MLORA_OK;
+}
+
+MxRows rows_of(const mlora_mx_matrix *Q)
+{
+    MxRows q;
+    q.codes = static_cast<uint8_t *>(Q->codes);
+    q.ld = Q->ld;
+    q.scales = static_cast<uint8_t *>(Q->scales);
+    q.n_rows = Q->n_rows;
+    q.n_cols = Q->n_cols;
+    q.chunks = (Q->n_cols + 255) / 256;
+    return q;
+}
+
+}  // namespace
+
+}  // namespace mlora
+
+using namespace mlora;
+
+// Sizes, strides and pointers of a quantised matrix (an empty one needs no memory).
+mlora_status mlora_mx_check_matrix(const mlora_mx_matrix *Q)
+{
+    if (Q->n_rows < 0 || Q->n_cols <= 0) return MLORA_ERR_INVALID_ARG;
+    if (Q->n_cols % 8 != 0) return MLORA_ERR_UNSUPPORTED;
+    if (Q->ld % 16 != 0 || Q->ld < ((int64_t)Q->n_cols + 31) / 32 * 16) return MLORA_ERR_INVALID_ARG;
+    if (Q->n_rows > 0 && (Q->codes == nullptr || Q->scales == nullptr || !aligned16(Q->codes) || !aligned16(Q->scales)))
+        return MLORA_ERR_INVALID_ARG;
+    return MLORA_OK;
+}
+
+extern "C" {
+
+int64_t mlora_mx_scale_bytes(int32_t n_rows, int32_t n_cols)
+{
+    if (n_rows < 0 || n_cols < 0) return -1;
+    return ((int64_t)n_rows + 127) / 128 * (((int64_t)n_cols + 255) / 256) * 1024;
+}
+
+mlora_status mlora_mx_quantize(const void *X, int32_t x_dtype, int64_t ldx, const mlora_mx_matrix *Q, void *stream)
+{
+    bool empty = false;
+    mlora_status st = check_operand(X, x_dtype, ldx, Q, empty);
+    if (st != MLORA_OK || empty) return st;
+    const MxRows q = rows_of(Q);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned b = quant_blocks(q);
+    if (x_dtype == MLORA_DTYPE_BF16)
+        mx_quantize_kernel<<<b, kQuantThreads, 0, s>>>(static_cast<const __nv_bfloat16 *>(X), ldx, q);
+    else if (x_dtype == MLORA_DTYPE_FP16)
+        mx_quantize_kernel<<<b, kQuantThreads, 0, s>>>(static_cast<const __half *>(X), ldx, q);
+    else
+        mx_quantize_kernel<<<b, kQuantThreads, 0, s>>>(static_cast<const float *>(X), ldx, q);
+    return cudaGetLastError() == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
+}
+
+mlora_status mlora_mx_dequantize(const mlora_mx_matrix *Q, void *X, int32_t x_dtype, int64_t ldx, void *stream)
+{
+    bool empty = false;
+    mlora_status st = check_operand(X, x_dtype, ldx, Q, empty);
+    if (st != MLORA_OK || empty) return st;
+    const MxRows q = rows_of(Q);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const unsigned b = quant_blocks(q);
+    if (x_dtype == MLORA_DTYPE_BF16)
+        mx_dequantize_kernel<<<b, kQuantThreads, 0, s>>>(q, static_cast<__nv_bfloat16 *>(X), ldx);
+    else if (x_dtype == MLORA_DTYPE_FP16)
+        mx_dequantize_kernel<<<b, kQuantThreads, 0, s>>>(q, static_cast<__half *>(X), ldx);
+    else
+        mx_dequantize_kernel<<<b, kQuantThreads, 0, s>>>(q, static_cast<float *>(X), ldx);
+    return cudaGetLastError() == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -671,3 +671,76 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cluster_addr, uint32_t v
 }
 
 }  // namespace mlora
+
+// ---------------------------------------------------------------- 4-bit e2m1 values
+namespace mlora {
+
+// Eight fp32 values as e2m1 codes (round to nearest even, saturating), the first in the
+// lowest four bits.
+__device__ __forceinline__ uint32_t e2m1x8(float a0, float a1, float a2, float a3, float a4, float a5, float a6,
+                                           float a7)
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}\n"
+        : "=r"(r)
+        : "f"(a0), "f"(a1), "f"(a2), "f"(a3), "f"(a4), "f"(a5), "f"(a6), "f"(a7));
+    return r;
+}
+
+// The eight values of e2m1 codes (all exact in fp16).
+__device__ __forceinline__ void e2m1x8_to_float(uint32_t c, float (&f)[8])
+{
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(c));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        asm("{\n\t.reg .b16 l, u;\n\tmov.b32 {l, u}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}\n"
+            : "=f"(f[2 * i]), "=f"(f[2 * i + 1])
+            : "r"(h[i]));
+    }
+}
+
+// ---------------------------------------------------------------- block-scaled 4-bit MMA
+// Instruction descriptor for kind::mxf4 (A and B e2m1, K-major, K = 64; D fp32; scales
+// e8m0, one per 32 elements of K).  sfa / sfb: which byte pair (0 or 2) of each 32-bit
+// tensor-memory word of scales the instruction uses.
+__host__ __device__ constexpr uint32_t umma_idesc_mxf4(int m, int n, int sfa, int sfb)
+{
+    return ((uint32_t)sfb << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) |
+           ((uint32_t)(m >> 7) << 27) | ((uint32_t)sfa << 29);
+}
+
+// D[tmem] (+)= (A scaled) (B scaled)^T, operands in shared memory, scales in tensor memory.
+__device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        : "memory");
+}
+
+// 32 rows x 16 bytes of shared memory (rows 16 bytes apart) to four tensor-memory columns,
+// row i to lane i of all four lane quarters: one 512-byte tile of scales.
+__device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem_byte_addr)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
+                 ::"r"(taddr), "l"(umma_desc_kmajor(smem_byte_addr, 128, 128))
+                 : "memory");
+}
+
+}  // namespace mlora
