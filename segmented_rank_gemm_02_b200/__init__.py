@@ -156,9 +156,10 @@ def _ptr(x) -> Optional[int]:
 
 
 def _ld(t, what: str) -> int:
-    if t.dim() != 2 or t.stride(1) != 1:
+    st = t.stride()
+    if len(st) != 2 or st[1] != 1:
         raise ValueError(f"{what} must be a 2-D row-major tensor")
-    return int(t.stride(0))
+    return int(st[0])
 
 
 def as_bf16_tensor(bits: np.ndarray, device=None):
@@ -367,20 +368,69 @@ def expand(pool: Pool, segs: DeviceSegments, H, Y, stream=None) -> None:
                              _ptr(Y), _ld(Y, "Y"), _stream_ptr(stream)), "mlora_expand")
 
 
+_float_codes = {}   # torch dtype -> MLORA_DTYPE_* of the types rows and outputs may have
+
+
+def _float_code(t, what: str) -> int:
+    if not _float_codes:
+        import torch
+        _float_codes.update({torch.bfloat16: DTYPE_BF16, torch.float16: DTYPE_FP16, torch.float32: DTYPE_FP32})
+    code = _float_codes.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{what} must be bf16, fp16 or fp32")
+    return code
+
+
+def _call(fn, what: str, device: int, stream, *args) -> None:
+    """fn(*args, stream) with `device` current, on its current stream unless one is given."""
+    import torch
+    if device < 0:
+        raise ValueError("the tensors must be on a CUDA device")
+    if device != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return _call(fn, what, device, stream, *args)
+    # (the raw handle: making a Stream object costs more than the call)
+    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream_ptr(stream)
+    st = fn(*args, s)
+    if st != OK:
+        raise MloraError(st, what)
+
+
+def _empty(shape, dtype, device, stream):
+    """An output for a call on `stream`: allocated there, so that its memory is not still in use elsewhere."""
+    import torch
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 class MxMatrix:
     """A 4-bit microscaled matrix (mlora_mx_matrix): packed codes [n_rows, 16 per block of 32
     columns] and scale tiles [ceil(n_rows / 128), 2 ceil(n_cols / 256), 32, 4, 4], uint8, allocated
     on `device` or given (a checkpoint's own, already in this layout)."""
 
-    def __init__(self, n_rows: int, n_cols: int, device=None, codes=None, scales=None):
+    def __init__(self, n_rows: int, n_cols: int, device=None, codes=None, scales=None, stream=None):
         import torch
         n_rows, n_cols = int(n_rows), int(n_cols)
         if n_rows < 0 or n_cols <= 0 or n_cols % 8 != 0:
             raise ValueError("a 4-bit matrix has n_rows >= 0 and n_cols a positive multiple of 8")
         row_bytes = (n_cols + 31) // 32 * 16
-        shape = ((n_rows + 127) // 128, 2 * ((n_cols + 255) // 256), 32, 4, 4)
+        self.n_rows, self.n_cols = n_rows, n_cols
+        self._codes, self._scales = codes, scales
+        if codes is None and scales is None:
+            # one allocation: the scale tiles (whole 1 KB), then the codes; the tensors are made when asked for
+            at = (n_rows + 127) // 128 * ((n_cols + 255) // 256) * 1024
+            self._buf = _empty(at + n_rows * row_bytes, torch.uint8, device, stream)
+            ptr = self._buf.data_ptr()
+            self._index = self._buf.get_device()
+            self.struct = MxStruct(n_rows, n_cols, row_bytes, ptr + at, ptr)
+            return
+        shape = self._scale_shape()
         if codes is None:
-            codes = torch.empty((n_rows, row_bytes), dtype=torch.uint8, device=device)
+            codes = torch.empty((n_rows, row_bytes), dtype=torch.uint8, device=scales.device)
         if scales is None:
             scales = torch.empty(shape, dtype=torch.uint8, device=codes.device)
         if codes.dtype != torch.uint8 or tuple(codes.shape) != (n_rows, row_bytes):
@@ -389,56 +439,58 @@ class MxMatrix:
             raise ValueError(f"scales must be contiguous uint8 {list(shape)}")
         if scales.device != codes.device:
             raise ValueError("codes and scales must be on one device")
-        self.codes, self.scales = codes, scales
-        self.n_rows, self.n_cols = n_rows, n_cols
+        self._codes, self._scales = codes, scales
+        self._index = codes.get_device()
         self.struct = MxStruct(n_rows, n_cols, _ld(codes, "codes") if n_rows > 1 else row_bytes, _ptr(codes),
                                _ptr(scales))
 
+    def _scale_shape(self):
+        return ((self.n_rows + 127) // 128, 2 * ((self.n_cols + 255) // 256), 32, 4, 4)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            rows = self.n_rows * ((self.n_cols + 31) // 32 * 16)
+            self._codes = self._buf[self._buf.numel() - rows:].view(self.n_rows, (self.n_cols + 31) // 32 * 16)
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            shape = self._scale_shape()
+            self._scales = self._buf[:shape[0] * shape[1] * 512].view(shape)
+        return self._scales
+
     @property
     def device(self):
-        return self.codes.device
-
-
-def _on_device(t, what: str):
-    """The device of a CUDA tensor, made current for the call (its stream is that device's)."""
-    import torch
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be on a CUDA device")
-    return torch.cuda.device(t.device)
-
-
-def _float_code(t, what: str) -> int:
-    code = _dtype_code(t)
-    if code == DTYPE_FP8_E4M3:
-        raise ValueError(f"{what} must be bf16, fp16 or fp32")
-    return code
+        return (self._buf if self._codes is None else self._codes).device
 
 
 def mx_quantize(X, out: Optional[MxMatrix] = None, stream=None) -> MxMatrix:
     """X [n, d] (bf16, fp16 or fp32, on the GPU) as a 4-bit microscaled matrix (mlora_mx_quantize)."""
-    code = _float_code(X, "X")
-    ld = _ld(X, "X")
-    n, d = X.shape
-    with _on_device(X, "X"):
-        if out is None:
-            out = MxMatrix(n, d, X.device)
-        elif (out.n_rows, out.n_cols, out.device) != (n, d, X.device):
-            raise ValueError("out must have X's shape and device")
-        _check(lib().mlora_mx_quantize(_ptr(X), code, ld, ctypes.byref(out.struct), _stream_ptr(stream)),
-               "mlora_mx_quantize")
+    code, (n, d), ld, index = _float_code(X, "X"), X.shape, _ld(X, "X"), X.get_device()
+    if index < 0:
+        raise ValueError("X must be on a CUDA device")
+    if out is None:
+        out = MxMatrix(n, d, X.device, stream=stream)
+    elif (out.n_rows, out.n_cols, out._index) != (n, d, index):
+        raise ValueError("out must have X's shape and device")
+    _call(lib().mlora_mx_quantize, "mlora_mx_quantize", index, stream, X.data_ptr(), code,
+          ld if n > 1 else max(ld, d), ctypes.byref(out.struct))
     return out
 
 
 def mx_dequantize(Q: MxMatrix, out=None, dtype=None, stream=None):
     """The values Q stands for, in `dtype` (bf16 unless given) or into `out` (mlora_mx_dequantize)."""
     import torch
-    with _on_device(Q.codes, "Q"):
-        if out is None:
-            out = torch.empty((Q.n_rows, Q.n_cols), dtype=dtype or torch.bfloat16, device=Q.device)
-        elif tuple(out.shape) != (Q.n_rows, Q.n_cols) or out.device != Q.device or dtype not in (None, out.dtype):
-            raise ValueError("out must have Q's shape and device, and dtype if both are given")
-        _check(lib().mlora_mx_dequantize(ctypes.byref(Q.struct), _ptr(out), _float_code(out, "out"), _ld(out, "out"),
-                                         _stream_ptr(stream)), "mlora_mx_dequantize")
+    shape = (Q.n_rows, Q.n_cols)
+    if out is None:
+        out = _empty(shape, dtype or torch.bfloat16, Q.device, stream)
+    elif tuple(out.shape) != shape or out.get_device() != Q._index or dtype not in (None, out.dtype):
+        raise ValueError("out must have Q's shape and device, and dtype if both are given")
+    ld = _ld(out, "out")
+    _call(lib().mlora_mx_dequantize, "mlora_mx_dequantize", Q._index, stream, ctypes.byref(Q.struct), out.data_ptr(),
+          _float_code(out, "out"), ld if Q.n_rows > 1 else max(ld, Q.n_cols))
     return out
 
 
@@ -446,17 +498,23 @@ def mx_gemm_apply(pool: Pool, segs: Optional["DeviceSegments"], X, Xq: MxMatrix,
     """Y = round(Xq W^T + s (X A^T) B^T) for adapter rows, round(Xq W^T) for the others, in one pass
     (mlora_mx_gemm_apply).  Xq [n_rows, d_in] and W [d_out, d_in] 4-bit, X the bf16 activations that
     Xq was quantised from (not read, and may be None, if segs is None), Y bf16, fp16 or fp32."""
-    if tuple(Y.shape) != (Xq.n_rows, pool.d_out):
+    n, index = Xq.n_rows, Y.get_device()
+    if tuple(Y.shape) != (n, pool.d_out):
         raise ValueError("Y must be [rows of Xq, d_out]")
-    if segs is not None and (X is None or tuple(X.shape) != (Xq.n_rows, pool.d_in) or _dtype_code(X) != DTYPE_BF16):
-        raise ValueError("X must be bf16 [rows of Xq, d_in]")
-    if not (Xq.device == W.device == Y.device and (X is None or X.device == Y.device)):
-        raise ValueError("X, Xq, W and Y must be on one device")
-    with _on_device(Y, "Y"):
-        _check(lib().mlora_mx_gemm_apply(pool.handle, ctypes.byref(segs.struct) if segs is not None else None,
-                                         _ptr(X), _ld(X, "X") if X is not None else 0, ctypes.byref(Xq.struct),
-                                         ctypes.byref(W.struct), _ptr(Y), _float_code(Y, "Y"), _ld(Y, "Y"),
-                                         _stream_ptr(stream)), "mlora_mx_gemm_apply")
+    xp, ldx = None, 0
+    if segs is not None:
+        if X is None or tuple(X.shape) != (n, pool.d_in) or _float_code(X, "X") != DTYPE_BF16:
+            raise ValueError("X must be bf16 [rows of Xq, d_in]")
+        if X.get_device() != index:
+            raise ValueError("X and Y must be on one device")
+        xp, ldx = X.data_ptr(), _ld(X, "X")
+        ldx = ldx if n > 1 else max(ldx, pool.d_in)
+    if Xq._index != index or W._index != index:
+        raise ValueError("Xq, W and Y must be on one device")
+    ldy = _ld(Y, "Y")
+    _call(lib().mlora_mx_gemm_apply, "mlora_mx_gemm_apply", index, stream, pool.handle,
+          ctypes.byref(segs.struct) if segs is not None else None, xp, ldx, ctypes.byref(Xq.struct),
+          ctypes.byref(W.struct), Y.data_ptr(), _float_code(Y, "Y"), ldy if n > 1 else max(ldy, pool.d_out))
 
 
 class RowGroups:
@@ -465,22 +523,43 @@ class RowGroups:
 
     offsets, slots, ranks, order, positions: int32 device tensors (see mlora.h)."""
 
-    def __init__(self, pool: Pool, n_rows: int, top_k: int, device, max_segment_rows: int = 0):
+    def __init__(self, pool: Pool, n_rows: int, top_k: int, device, max_segment_rows: int = 0, stream=None):
         import torch
         n = n_rows * top_k
         S = min(pool.n_slots + 1, n)
-        buf = torch.empty(3 * S + 1 + 2 * n, dtype=torch.int32, device=device)
-        self.offsets, self.slots, self.ranks, self.order, self.positions = torch.split(buf, [S + 1, S, S, n, n])
-        self.pool, self.n_rows, self.top_k = pool, n_rows, top_k
-        at = buf.data_ptr()
-        self._out = RowGroupsStruct(at, at + 4 * (S + 1), at + 4 * (2 * S + 1), at + 4 * (3 * S + 1),
-                                    at + 4 * (3 * S + 1 + n))
-        self.struct = SegmentsStruct(S, n, n, int(max_segment_rows), self._out.offsets, self._out.slots,
-                                     self._out.ranks, None, self._out.order if top_k == 1 else None, None)
+        self.pool, self.n_rows, self.top_k, self.n_tokens, self._S = pool, n_rows, top_k, n, S
+        # one allocation; the tensors are made when asked for
+        self._buf = _empty(3 * S + 1 + 2 * n, torch.int32, device, stream)
+        self._index = self._buf.get_device()
+        at = self._buf.data_ptr()
+        offsets, slots, ranks, order, self._positions = at, at + 4 * (S + 1), at + 4 * (2 * S + 1), at + 4 * (
+            3 * S + 1), at + 4 * (3 * S + 1 + n)
+        self._out = RowGroupsStruct(offsets, slots, ranks, order, self._positions)
+        self.struct = SegmentsStruct(S, n, n, int(max_segment_rows), offsets, slots, ranks, None,
+                                     order if top_k == 1 else None, None)
+
+    def _part(self, first: int, count: int):
+        return self._buf[first:first + count]
 
     @property
-    def n_tokens(self) -> int:
-        return self.n_rows * self.top_k
+    def offsets(self):
+        return self._part(0, self._S + 1)
+
+    @property
+    def slots(self):
+        return self._part(self._S + 1, self._S)
+
+    @property
+    def ranks(self):
+        return self._part(2 * self._S + 1, self._S)
+
+    @property
+    def order(self):
+        return self._part(3 * self._S + 1, self.n_tokens)
+
+    @property
+    def positions(self):
+        return self._part(3 * self._S + 1 + self.n_tokens, self.n_tokens)
 
 
 def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segment_rows: int = 0,
@@ -489,68 +568,64 @@ def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segme
     [n_rows, top_k], contiguous, -1 = base model.  `out` reuses a RowGroups of the same sizes (a
     captured graph's).  max_segment_rows: the hint of mlora_segments, if the caller knows one."""
     import torch
-    if row_slots.dtype != torch.int32 or row_slots.dim() not in (1, 2) or not row_slots.is_contiguous():
+    shape = row_slots.shape
+    if row_slots.dtype != torch.int32 or len(shape) not in (1, 2) or not row_slots.is_contiguous():
         raise ValueError("row_slots must be contiguous int32 [n_rows] or [n_rows, top_k]")
-    n_rows = row_slots.shape[0]
-    top_k = 1 if row_slots.dim() == 1 else row_slots.shape[1]
-    if top_k < 1:
-        raise ValueError("row_slots needs at least one slot per row")
-    with _on_device(row_slots, "row_slots"):
-        if out is None:
-            out = RowGroups(pool, n_rows, top_k, row_slots.device, max_segment_rows)
-        elif (out.pool is not pool or (out.n_rows, out.top_k) != (n_rows, top_k)
-              or out.offsets.device != row_slots.device):
-            raise ValueError("out must be of this pool, the same sizes and device")
-        _check(lib().mlora_group_rows(pool.handle, _ptr(row_slots), n_rows, top_k, ctypes.byref(out._out),
-                                      _stream_ptr(stream)), "mlora_group_rows")
+    n_rows, top_k, index = shape[0], 1 if len(shape) == 1 else shape[1], row_slots.get_device()
+    if top_k < 1 or index < 0:
+        raise ValueError("row_slots needs at least one slot per row, on a CUDA device")
+    if out is None:
+        out = RowGroups(pool, n_rows, top_k, row_slots.device, max_segment_rows, stream)
+    elif out.pool is not pool or (out.n_rows, out.top_k, out._index) != (n_rows, top_k, index):
+        raise ValueError("out must be of this pool, the same sizes and device")
+    _call(lib().mlora_group_rows, "mlora_group_rows", index, stream, pool.handle, row_slots.data_ptr(), n_rows, top_k,
+          ctypes.byref(out._out))
     return out
 
 
-def _rows_of(t, n: int, like, what: str):
-    if t.dim() != 2 or t.shape[0] != n or (like is not None and (t.shape[1], t.dtype, t.device) != (
-            like.shape[1], like.dtype, like.device)):
+def _rows_of(t, n: int, d, dtype, index: int, what: str):
+    """Row stride of a [n, d] operand; its dtype and device must be these."""
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != n or shape[1] != d or t.dtype != dtype or t.get_device() != index:
         raise ValueError(f"{what} has the wrong shape, dtype or device")
-    return _ld(t, what) if n > 1 else max(int(t.stride(0)), int(t.shape[1]))
+    ld = _ld(t, what)
+    return ld if n > 1 else max(ld, d)
 
 
-def _weights_ptr(groups: RowGroups, w, device, what: str):
+def _weights_ptr(groups: RowGroups, w, index: int, what: str):
     import torch
     if w is None:
         return None
-    if w.dtype != torch.float32 or w.numel() != groups.n_tokens or not w.is_contiguous() or w.device != device:
+    if w.dtype != torch.float32 or w.numel() != groups.n_tokens or not w.is_contiguous() or w.get_device() != index:
         raise ValueError(f"{what} must be contiguous fp32 [n_rows, top_k] on the rows' device")
-    return _ptr(w)
+    return w.data_ptr()
 
 
 def gather_rows(groups: RowGroups, X, Xs=None, stream=None):
     """Xs[positions[t, j]] = X[t]: the rows in grouped order (mlora_gather_rows).  The gradient of X
     is combine_rows(groups, dXs)."""
-    import torch
-    code = _float_code(X, "X")
-    ldx = _rows_of(X, groups.n_rows, None, "X")
-    with _on_device(X, "X"):
-        if Xs is None:
-            Xs = torch.empty((groups.n_tokens, X.shape[1]), dtype=X.dtype, device=X.device)
-        ldxs = _rows_of(Xs, groups.n_tokens, X, "Xs")
-        _check(lib().mlora_gather_rows(groups.pool.handle, _ptr(groups.positions), groups.n_rows, groups.top_k, _ptr(X),
-                                       ldx, code, X.shape[1], groups.n_tokens, _ptr(Xs), ldxs, _stream_ptr(stream)),
-               "mlora_gather_rows")
+    code, d, n, index = _float_code(X, "X"), X.shape[-1], groups.n_tokens, groups._index
+    ldx = _rows_of(X, groups.n_rows, d, X.dtype, index, "X")
+    if Xs is None:
+        Xs, ldxs = _empty((n, d), X.dtype, X.device, stream), d
+    else:
+        ldxs = _rows_of(Xs, n, d, X.dtype, index, "Xs")
+    _call(lib().mlora_gather_rows, "mlora_gather_rows", index, stream, groups.pool.handle, groups._positions,
+          groups.n_rows, groups.top_k, X.data_ptr(), ldx, code, d, n, Xs.data_ptr(), ldxs)
     return Xs
 
 
 def combine_rows(groups: RowGroups, Ys, weights=None, Y=None, stream=None):
     """Y[t] = sum_j weights[t, j] Ys[positions[t, j]] (mlora_combine_rows); weights fp32 or None (ones)."""
-    import torch
-    code = _float_code(Ys, "Ys")
-    ldys = _rows_of(Ys, groups.n_tokens, None, "Ys")
-    w = _weights_ptr(groups, weights, Ys.device, "weights")
-    with _on_device(Ys, "Ys"):
-        if Y is None:
-            Y = torch.empty((groups.n_rows, Ys.shape[1]), dtype=Ys.dtype, device=Ys.device)
-        ldy = _rows_of(Y, groups.n_rows, Ys, "Y")
-        _check(lib().mlora_combine_rows(groups.pool.handle, _ptr(groups.positions), w, groups.n_rows, groups.top_k,
-                                        _ptr(Ys), ldys, code, Ys.shape[1], groups.n_tokens, _ptr(Y), ldy,
-                                        _stream_ptr(stream)), "mlora_combine_rows")
+    code, d, n, index = _float_code(Ys, "Ys"), Ys.shape[-1], groups.n_tokens, groups._index
+    ldys = _rows_of(Ys, n, d, Ys.dtype, index, "Ys")
+    w = _weights_ptr(groups, weights, index, "weights")
+    if Y is None:
+        Y, ldy = _empty((groups.n_rows, d), Ys.dtype, Ys.device, stream), d
+    else:
+        ldy = _rows_of(Y, groups.n_rows, d, Ys.dtype, index, "Y")
+    _call(lib().mlora_combine_rows, "mlora_combine_rows", index, stream, groups.pool.handle, groups._positions, w,
+          groups.n_rows, groups.top_k, Ys.data_ptr(), ldys, code, d, n, Y.data_ptr(), ldy)
     return Y
 
 
@@ -558,23 +633,22 @@ def combine_rows_backward(groups: RowGroups, dY, Ys, weights=None, dYs=None, dwe
     """(dYs, dweights) of combine_rows from dY (mlora_combine_rows_backward).  Without weights only dYs
     is computed (dweights is None, Ys may be None) unless a dweights tensor is given."""
     import torch
-    code = _float_code(dY, "dY")
-    lddy = _rows_of(dY, groups.n_rows, None, "dY")
-    w = _weights_ptr(groups, weights, dY.device, "weights")
-    with _on_device(dY, "dY"):
-        if dYs is None:
-            dYs = torch.empty((groups.n_tokens, dY.shape[1]), dtype=dY.dtype, device=dY.device)
-        lddys = _rows_of(dYs, groups.n_tokens, dY, "dYs")
-        if dweights is None and weights is not None:
-            dweights = torch.empty((groups.n_rows, groups.top_k), dtype=torch.float32, device=dY.device)
-        dw = _weights_ptr(groups, dweights, dY.device, "dweights")
-        if dw is not None and Ys is None:
-            raise ValueError("the gradient of the weights needs Ys")
-        ldys = _rows_of(Ys, groups.n_tokens, dY, "Ys") if Ys is not None else 0
-        _check(lib().mlora_combine_rows_backward(groups.pool.handle, _ptr(groups.positions), w, groups.n_rows,
-                                                 groups.top_k, _ptr(dY), lddy, _ptr(Ys), ldys, code, dY.shape[1],
-                                                 groups.n_tokens, _ptr(dYs), lddys, dw, _stream_ptr(stream)),
-               "mlora_combine_rows_backward")
+    code, d, n, index = _float_code(dY, "dY"), dY.shape[-1], groups.n_tokens, groups._index
+    lddy = _rows_of(dY, groups.n_rows, d, dY.dtype, index, "dY")
+    w = _weights_ptr(groups, weights, index, "weights")
+    if dYs is None:
+        dYs, lddys = _empty((n, d), dY.dtype, dY.device, stream), d
+    else:
+        lddys = _rows_of(dYs, n, d, dY.dtype, index, "dYs")
+    if dweights is None and weights is not None:
+        dweights = _empty((groups.n_rows, groups.top_k), torch.float32, dY.device, stream)
+    dw = _weights_ptr(groups, dweights, index, "dweights")
+    if dw is not None and Ys is None:
+        raise ValueError("the gradient of the weights needs Ys")
+    ysp, ldys = (None, 0) if Ys is None else (Ys.data_ptr(), _rows_of(Ys, n, d, dY.dtype, index, "Ys"))
+    _call(lib().mlora_combine_rows_backward, "mlora_combine_rows_backward", index, stream, groups.pool.handle,
+          groups._positions, w, groups.n_rows, groups.top_k, dY.data_ptr(), lddy, ysp, ldys, code, d, n, dYs.data_ptr(),
+          lddys, dw)
     return dYs, dweights
 
 

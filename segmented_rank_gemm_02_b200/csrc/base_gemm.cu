@@ -140,22 +140,6 @@ __device__ __forceinline__ uint32_t leader_bar(const uint64_t *bar) { return map
 }  // namespace
 
 // ------------------------------------------------------------------ row map
-// The problems of segment g (status bits as the other kernels report them), 0 if it
-// is a valid adapter segment; *rank and *scale are set for a valid one.
-__device__ __forceinline__ unsigned segment_problem(const TileParams &p, int g, int a, int p0, int p1, int &rank,
-                                                    float &scale)
-{
-    if (a < -1 || a >= p.n_slots) return kFlagBadSlot;
-    if (p0 < 0 || p1 < p0 || p1 > p.n_tokens) return kFlagBadOffsets;
-    if (a < 0) return 0;
-    rank = p.slot_rank[a];
-    scale = p.scales ? p.scales[g] : p.slot_scale[a];
-    if (p.generations && p.slot_gen[a] != p.generations[g]) return kFlagStaleSlot;
-    if (rank <= 0) return kFlagSlotEmpty;
-    if ((p.ranks && p.ranks[g] != rank) || rank_bucket(rank) == 0) return kFlagBadRank;
-    return 0;
-}
-
 // Grid-stride over segments (their problems are reported once each) and over
 // grouped positions: position q belongs to the segment g with offsets[g] <= q <
 // offsets[g + 1] (binary search over the offsets); when that segment is a valid
@@ -174,13 +158,7 @@ __global__ void __launch_bounds__(256) row_map_kernel(const __grid_constant__ Ti
     }
     if (p.n_segments <= 0) return;
     for (int q = i0; q < p.n_tokens; q += stride) {
-        int lo = 0, hi = p.n_segments - 1;   // last g with offsets[g] <= q
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.offsets[mid] <= q) lo = mid;
-            else hi = mid - 1;
-        }
-        const int g = lo, a = p.slots[g], p0 = p.offsets[g], p1 = p.offsets[g + 1];
+        const int g = segment_of_position(p, q), a = p.slots[g], p0 = p.offsets[g], p1 = p.offsets[g + 1];
         if (a < 0 || q < p0 || q >= p1) continue;
         int rank = 0;
         float scale = 0.f;
@@ -196,9 +174,8 @@ __global__ void __launch_bounds__(256) row_map_kernel(const __grid_constant__ Ti
     }
 }
 
-// One CTA of PM threads per PM-row block (PM = 128 or 256): the distinct slots of the block's rows in
+// One CTA of 256 threads per 256-row block: the distinct slots of the block's rows in
 // order of first appearance, as out[0] = count, then (slot, rank bucket) pairs.
-template <int PM>
 __global__ void __launch_bounds__(PM) block_slots_kernel(const int4 *row_info, int n_rows, int32_t *out)
 {
     __shared__ int s_slot[PM];
@@ -560,13 +537,11 @@ cudaError_t launch_row_map(const TileParams &p, int4 *row_info, cudaStream_t str
     return cudaGetLastError();
 }
 
-cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream,
-                               int block_rows)
+cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream)
 {
-    const int n_mblk = (n_rows + block_rows - 1) / block_rows;
+    const int n_mblk = (n_rows + PM - 1) / PM;
     if (n_mblk <= 0) return cudaSuccess;
-    if (block_rows == 128) block_slots_kernel<128><<<n_mblk, 128, 0, stream>>>(row_info, n_rows, block_slots);
-    else block_slots_kernel<PM><<<n_mblk, PM, 0, stream>>>(row_info, n_rows, block_slots);
+    block_slots_kernel<<<n_mblk, PM, 0, stream>>>(row_info, n_rows, block_slots);
     return cudaGetLastError();
 }
 

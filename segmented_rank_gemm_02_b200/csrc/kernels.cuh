@@ -206,9 +206,8 @@ struct GemmParams {
 // row_info for every row (memset to -1, then the valid segments' rows); reports the
 // segments' problems in p.status.
 cudaError_t launch_row_map(const TileParams &p, int4 *row_info, cudaStream_t stream);
-// The distinct slots of each block of `block_rows` rows (256 or 128).
-cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream,
-                               int block_rows = kGemmRows);
+// The distinct slots of each 256-row block of rows.
+cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream);
 // Tile width (256 or 512 columns of Y) for n_mblk 256-row blocks and d_out columns.
 int choose_gemm_cols(int n_mblk, int d_out);
 // Persistent GEMM over all (256-row, gn-column) tiles, one pair of CTAs per two SMs;
@@ -219,27 +218,49 @@ cudaError_t prepare_base_gemm();
 
 // ---- 4-bit base GEMM + LoRA (mx_gemm.cu)
 
-constexpr int kMxTileRows = 128;   // rows of Y per tile (and per block of slot lists)
+constexpr int kMxTileRows = 128;   // rows of Y per CTA
 
-// Everything one launch of the 4-bit GEMM needs.  Passed by value.
+// What every launch of the 4-bit GEMM needs.  Passed by value.
 struct MxGemmParams {
     CUtensorMap x_map, w_map;   // codes as bytes [rows][row bytes], box 128 x 128, 128-byte swizzle
+    CUtensorMap xs_map, ws_map; // scale tiles as 32-bit words [128-row blocks][256 per 256 columns], box 256 x 1
     CUtensorMap b_map[4];       // the pool's B blocks, as in GemmParams
     int32_t b_col_div;
-    const uint8_t *x_scales, *w_scales;   // scale tiles, 1 KB per 128 rows and 256 columns
-    const int4 *row_info;       // as in GemmParams; unused without LoRA
-    const int32_t *block_slots; // [n_mblk][kBlockSlotsPitch], blocks of kMxTileRows rows
-    const float *H;
-    int64_t ldh;
     void *Y;                    // [n_rows][ldy], written for every row
     int64_t ldy;
     int32_t y_type;             // 0 bf16, 1 fp16, 2 fp32
     unsigned int *status;
-    int32_t n_rows, d_in, d_out, n_mblk, n_nblk;
+    int32_t n_rows, d_in, d_out, n_mblk, n_nblk;   // row and column blocks of the form's tiles
 };
 
+// The few-rows form finds its rows' segments itself; t: pool, segments and status (unused
+// without LoRA, as H is).
+struct MxSegments {
+    TileParams t;
+    const float *H;             // [n_tokens][ldh] fp32, grouped order (the shrink's output)
+    int64_t ldh;
+};
+
+// The many-rows form reads them from row_info and the 256-row blocks' slot lists, as GemmParams.
+struct MxSlots {
+    const int4 *row_info;
+    const int32_t *block_slots;
+    const float *H;
+    int64_t ldh;
+};
+
+struct MxPlan {
+    int tile;      // 1: the few-rows form (128 x 128 tiles), 0: the many-rows one (256 x 256 pair tiles)
+    int ksplit;    // CTAs per tile of the few-rows form
+};
+MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out);
+
 // Y = X W^T (+ the slots' low-rank products if rank_bucket_max > 0, the pool's largest bucket).
-cudaError_t launch_mx_gemm(const MxGemmParams &p, int rank_bucket_max, cudaStream_t stream);
+// Both launch with programmatic dependent launch: they read nothing before the kernels that the
+// one before them in the stream waited for, and that one itself, are complete.
+cudaError_t launch_mx_tile(const MxGemmParams &p, const MxSegments &sg, int rank_bucket_max, int ksplit,
+                           cudaStream_t stream);
+cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int rank_bucket_max, cudaStream_t stream);
 cudaError_t prepare_mx_gemm();
 
 // ---- rows grouped by slot (rows.cu)

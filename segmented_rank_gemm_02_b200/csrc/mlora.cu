@@ -173,6 +173,22 @@ bool encode_codes_map(CUtensorMap *map, const void *base, int64_t rows, int64_t 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Scale tiles as 32-bit words: per 128 rows one row of 256 words per 256 columns, box 256 x 1
+// (the two tiles of one K block); blocks past the last read as zeros.
+bool encode_scales_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols)
+{
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr || base == nullptr || rows <= 0 || cols <= 0) return false;
+    const cuuint64_t words = (cuuint64_t)((cols + 255) / 256) * 256;
+    cuuint64_t dims[2] = {words, (cuuint64_t)((rows + 127) / 128)};
+    cuuint64_t strides[1] = {words * 4};
+    cuuint32_t box[2] = {256, 1};
+    cuuint32_t elem[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, elem,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // The pool's B blocks as a 4-D tensor [slot][rank group][d_out][8] (bf16), box
 // {8, cols, R/8, 1}: one chunk of `cols` columns of one slot's B for rank bucket R.
 bool encode_b_map(CUtensorMap *map, const mlora_pool *pool, int R, int cols)
@@ -767,13 +783,15 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
     if (st != MLORA_OK) return st;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
 
+    const mlora::MxPlan plan = mlora::plan_mx_gemm(Xq->n_rows, pool->d_in, pool->d_out);
+    const int tile = plan.tile ? mlora::kMxTileRows : 2 * mlora::kMxTileRows;   // rows and columns of a tile
     mlora::MxGemmParams g{};
     const int64_t row_bytes = round_up(pool->d_in, 32) / 2;
     if (!encode_codes_map(&g.x_map, Xq->codes, Xq->n_rows, row_bytes, Xq->ld) ||
-        !encode_codes_map(&g.w_map, W->codes, W->n_rows, row_bytes, W->ld))
+        !encode_codes_map(&g.w_map, W->codes, W->n_rows, row_bytes, W->ld) ||
+        !encode_scales_map(&g.xs_map, Xq->scales, Xq->n_rows, pool->d_in) ||
+        !encode_scales_map(&g.ws_map, W->scales, W->n_rows, pool->d_in))
         return MLORA_ERR_CUDA;
-    g.x_scales = static_cast<const uint8_t *>(Xq->scales);
-    g.w_scales = static_cast<const uint8_t *>(W->scales);
     g.Y = Y;
     g.ldy = ldy;
     g.y_type = y_dtype;
@@ -781,39 +799,42 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
     g.n_rows = Xq->n_rows;
     g.d_in = pool->d_in;
     g.d_out = pool->d_out;
-    g.n_mblk = (Xq->n_rows + mlora::kMxTileRows - 1) / mlora::kMxTileRows;
-    g.n_nblk = (pool->d_out + 127) / 128;
-    if (!lora) return mlora::launch_mx_gemm(g, 0, cs) == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
+    g.n_mblk = (Xq->n_rows + tile - 1) / tile;
+    g.n_nblk = (pool->d_out + tile - 1) / tile;
+    if (!lora) {
+        const cudaError_t e = plan.tile ? mlora::launch_mx_tile(g, mlora::MxSegments{}, 0, plan.ksplit, cs)
+                                        : mlora::launch_mx_pair(g, mlora::MxSlots{}, 0, cs);
+        return e == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
+    }
+    for (int i = 0; i < 4; ++i) g.b_map[i] = pool->b_maps_wide_ok ? pool->b_maps_wide[i] : pool->b_maps[i];
+    g.b_col_div = pool->b_maps_wide_ok ? 32 : 1;
 
-    // workspace: H (grouped order), the row map, the slot lists of the row blocks
+    // workspace: H (grouped order); for the many-rows form the row map and the row blocks' slot lists
     const int rk = std::max(16, pool->r_bucket_max);
     const size_t h_bytes = (size_t)round_up((int64_t)segs->n_tokens * rk * 4, 256);
-    const size_t map_bytes = (size_t)round_up((int64_t)segs->n_rows * 16, 256);
-    const size_t slot_bytes = (size_t)g.n_mblk * mlora::kBlockSlotsPitch * 4;
+    const size_t map_bytes = plan.tile ? 0 : (size_t)round_up((int64_t)segs->n_rows * 16, 256);
+    const size_t slot_bytes = plan.tile ? 0 : (size_t)g.n_mblk * mlora::kBlockSlotsPitch * 4;
     std::lock_guard<std::mutex> lock(pool->ws_mutex);   // held until the kernels are launched
     st = ensure_workspace(pool, h_bytes + map_bytes + slot_bytes, cs);
     if (st != MLORA_OK) return st;
     uint8_t *ws = reinterpret_cast<uint8_t *>(pool->ws);
     float *H = reinterpret_cast<float *>(ws);
-    int4 *row_info = reinterpret_cast<int4 *>(ws + h_bytes);
-    int32_t *block_slots = reinterpret_cast<int32_t *>(ws + h_bytes + map_bytes);
     mlora::TileParams p = base_params(pool, segs);
     p.X = static_cast<const __nv_bfloat16 *>(X);
     p.ldx = ldx;
     p.H = H;
     p.ldh = rk;
-    if (mlora::launch_row_map(p, row_info, cs) != cudaSuccess ||
-        mlora::launch_block_slots(row_info, segs->n_rows, block_slots, cs, mlora::kMxTileRows) != cudaSuccess)
+    int4 *row_info = reinterpret_cast<int4 *>(ws + h_bytes);
+    int32_t *block_slots = reinterpret_cast<int32_t *>(ws + h_bytes + map_bytes);
+    if (!plan.tile && (mlora::launch_row_map(p, row_info, cs) != cudaSuccess ||
+                       mlora::launch_block_slots(row_info, segs->n_rows, block_slots, cs) != cudaSuccess))
         return MLORA_ERR_CUDA;
     st = launch(pool, segs, mlora::MODE_SHRINK, p, stream);
     if (st != MLORA_OK) return st;
-    for (int i = 0; i < 4; ++i) g.b_map[i] = pool->b_maps_wide_ok ? pool->b_maps_wide[i] : pool->b_maps[i];
-    g.b_col_div = pool->b_maps_wide_ok ? 32 : 1;
-    g.row_info = row_info;
-    g.block_slots = block_slots;
-    g.H = H;
-    g.ldh = rk;
-    return mlora::launch_mx_gemm(g, pool->r_bucket_max, cs) == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
+    const cudaError_t e =
+        plan.tile ? mlora::launch_mx_tile(g, mlora::MxSegments{p, H, rk}, pool->r_bucket_max, plan.ksplit, cs)
+                  : mlora::launch_mx_pair(g, mlora::MxSlots{row_info, block_slots, H, rk}, pool->r_bucket_max, cs);
+    return e == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
 }
 
 mlora_status mlora_apply_multi(mlora_pool *const *pools, int32_t n_proj, const mlora_segments *segs,

@@ -6,21 +6,15 @@
 // of the unquantised X comes from the library's segmented shrink, in fp32, as in
 // base_gemm.cu.  Products of codes are exact and sums are fp32 in the tensor core
 // (tcgen05.mma kind::mxf4, K = 64 per instruction, two scales per row and instruction); the
-// low-rank product is a second accumulator (kind::f16, s H split into bf16 hi + lo) and the
-// two are added in fp32 before the one rounding.
+// low-rank products (kind::f16, s H split into bf16 hi + lo) are added in fp32 before the one
+// rounding.
 //
-// Tile kernel: 128 rows x 128 columns of Y per cluster of `ksplit` CTAs, each CTA one part
-// of d_in and every ksplit-th of the tile's adapter slots.  Warp roles:
-//   warp 0     TMA: per 256-wide K block the codes of X and W (128 rows x 128 bytes each,
-//              128-byte swizzle) and their scale tiles (1 KB each) into a ring; after the K
-//              blocks the slots' B chunks
-//   warp 1     tensor memory; one thread copies a stage's scale tiles into that stage's own
-//              tensor-memory columns and issues the products
-//   warps 2-5  stage the slots' rows of s H, then the epilogue
-// With more than one CTA each leaves its fp32 part in shared memory; after a cluster
-// barrier every CTA sums a share of the columns over the cluster in CTA order.
-// Every mbarrier wait is bounded; on expiry the kernel flags a timeout and stores nothing.
+// Two kernels.  Few rows are bound by the bytes of W and by latency: mx_tile_kernel, 128 x 128
+// tiles with d_in split over a cluster, so that all SMs stream W.  Many rows are bound by the
+// tensor core and the copies that feed it: mx_pair_kernel, 256 x 256 tiles on pairs of CTAs.
+// Every mbarrier wait is bounded; on expiry a kernel flags a timeout and stores nothing.
 #include <algorithm>
+#include <mutex>
 
 #include <cuda_fp16.h>
 
@@ -32,48 +26,105 @@ namespace mlora {
 
 namespace {
 
-constexpr int MR = kMxTileRows;            // rows per tile
-constexpr int MC = 128;                    // columns per tile
+constexpr int MR = kMxTileRows;            // rows per CTA (one tensor-memory lane each)
 constexpr int KB = 256;                    // K per stage: 128 bytes of codes per row
-constexpr int OP_BYTES = MR * KB / 2;      // 16 KB: one operand's codes of a stage
-constexpr int SF_BYTES = 1024;             // one operand's scale tiles of a stage
-constexpr int STAGE = 2 * OP_BYTES + 2 * SF_BYTES;
-constexpr int MX_WARPS = 6;
-constexpr int MT = MX_WARPS * 32;
-constexpr int kMaxStages = 6;
-// tensor memory: accumulator, low-rank accumulator, 16 columns of scales per stage
-constexpr int T_LORA = 128, T_SCALES = 256, T_COLS = 512;
-constexpr int RED_PITCH = MC + 4;          // floats per row of the reduction buffer
+constexpr int OP_BYTES = 128 * KB / 2;     // 16 KB: the codes of 128 rows, one stage
+constexpr int SF_BYTES = 1024;             // their scale tiles (two of 512 bytes)
 constexpr uint64_t kMxWaitNs = 1000000000ull;
-constexpr int kRowBar = 1;
-
-// RK: 0 without LoRA, else 16 or 64, the largest rank bucket of the pool (at least 16).
-template <int RK>
-struct Shape {
-    static constexpr int HOP = MR * RK * 2;            // one of hi / lo
-    static constexpr int GS = RK == 64 ? 4 : 6;        // ring stages
-    static constexpr int ZERO = RK ? 2048 : 0;         // the zero second half of a rank-8 B chunk
-    static constexpr int SMEM = 1024 + GS * STAGE + 4 * HOP + ZERO;
-    static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
-    static_assert(MR * RED_PITCH * 4 <= GS * STAGE, "the reduction buffer reuses the ring");
-    static_assert(GS <= kMaxStages && T_SCALES + 16 * GS <= T_COLS, "tensor memory");
-    static_assert(STAGE % 1024 == 0 && MC * RK * 2 <= STAGE, "stage layout");
-};
-
-struct Ctl {
-    uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t done;                 // every product of the tile is in tensor memory
-    uint64_t hop_full[2], hop_empty[2];
-    uint32_t tmem;
-    volatile int fail;
-};
+constexpr int kRowBar = 1;                 // named barrier of the operand warps
+constexpr int kEpiBar = 2;                 // named barrier of the epilogue warps (pair kernel)
 
 __device__ __forceinline__ uint8_t *align_1024(uint8_t *p)
 {
     return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-__device__ __forceinline__ bool mwait(const MxGemmParams &p, Ctl &ctl, uint64_t *bar, uint32_t parity)
+// Two values as the 16-bit output type.
+template <int YT>
+__device__ __forceinline__ uint32_t pack2(float a, float b)
+{
+    if constexpr (YT == 1) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        return pack_bf16x2(a, b);
+    }
+}
+
+// Eight columns of a row, one rounding to the output's type.
+template <int YT>
+__device__ __forceinline__ void store8(const MxGemmParams &p, int row, int col, const float (&f)[8])
+{
+    const int64_t at = (int64_t)row * p.ldy + col;
+    if constexpr (YT == 2) {
+        float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(p.Y) + at);
+        y[0] = make_float4(f[0], f[1], f[2], f[3]);
+        y[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+        *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.Y) + at) =
+            make_uint4(pack2<YT>(f[0], f[1]), pack2<YT>(f[2], f[3]), pack2<YT>(f[4], f[5]), pack2<YT>(f[6], f[7]));
+    }
+}
+
+__device__ __forceinline__ void store8(const MxGemmParams &p, int row, int col, const float (&f)[8])
+{
+    if (p.y_type == 2) store8<2>(p, row, col, f);
+    else if (p.y_type == 1) store8<1>(p, row, col, f);
+    else store8<0>(p, row, col, f);
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------ few rows
+// 128 rows x 128 columns of Y per cluster of `ksplit` CTAs, each CTA one part of d_in and every
+// ksplit-th of the tile's adapter slots.  Warp roles:
+//   warp 0     TMA: per 256-wide K block the codes of X and W (128 rows x 128 bytes each,
+//              128-byte swizzle) and their scale tiles (1 KB each) into a ring; after the K
+//              blocks the slots' B chunks
+//   warp 1     tensor memory; one thread copies a stage's scale tiles into that stage's own
+//              tensor-memory columns and issues the products; the low-rank products have an
+//              accumulator of their own
+//   warps 2-5  find the tile's rows in the segments and its distinct slots (while the K blocks
+//              stream: no launch of its own), offer the rows' s H slot by slot, then the epilogue
+// With more than one CTA each leaves its fp32 part in shared memory; after a cluster
+// barrier every CTA sums a share of the columns over the cluster in CTA order.
+namespace {
+
+constexpr int MC = 128;                    // columns per tile
+constexpr int STAGE = 2 * OP_BYTES + 2 * SF_BYTES;
+constexpr int MT = 6 * 32;
+constexpr int kMaxStages = 6;
+// tensor memory: accumulator, low-rank accumulator, 16 columns of scales per stage
+constexpr int T_LORA = 128, T_SCALES = 256, T_COLS = 512;
+constexpr int RED_PITCH = MC + 4;          // floats per row of the reduction buffer
+
+// RK: 0 without LoRA, else 16 or 64, the largest rank bucket of the pool (at least 16).
+template <int RK>
+struct TileShape {
+    static constexpr int HOP = MR * RK * 2;            // one of hi / lo
+    static constexpr int GS = RK == 64 ? 4 : 6;        // ring stages
+    static constexpr int ZERO = RK ? 2048 : 0;         // the zero second half of a rank-8 B chunk
+    static constexpr int SMEM = 1024 + GS * STAGE + 4 * HOP + ZERO;
+    static_assert(SMEM + 4096 <= 227 * 1024, "shared memory");
+    static_assert(MR * RED_PITCH * 4 <= GS * STAGE, "the reduction buffer reuses the ring");
+    static_assert(GS <= kMaxStages && T_SCALES + 16 * GS <= T_COLS, "tensor memory");
+    static_assert(STAGE % 1024 == 0 && MC * RK * 2 <= STAGE, "stage layout");
+};
+
+struct TileCtl {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t done;                 // every product of the tile is in tensor memory
+    uint64_t hop_full[2], hop_empty[2];
+    uint64_t listed;               // the slot list is complete
+    uint32_t tmem;
+    volatile int fail;
+    int count;                     // distinct slots of the tile's rows, and their
+    int slot[MR], bucket[MR];      // numbers and rank buckets
+    int pos[MR], row_slot[MR];     // each row's grouped position (-1: none) and slot
+    int part[4];
+};
+
+__device__ __forceinline__ bool mwait(const MxGemmParams &p, TileCtl &ctl, uint64_t *bar, uint32_t parity)
 {
     if (ctl.fail) return false;
     if (!mbar_wait_bounded(bar, parity, kMxWaitNs)) {
@@ -84,38 +135,87 @@ __device__ __forceinline__ bool mwait(const MxGemmParams &p, Ctl &ctl, uint64_t 
     return true;
 }
 
-// Eight columns of a row, one rounding to the output's type.
-__device__ __forceinline__ void store8(const MxGemmParams &p, int row, int col, const float (&f)[8])
+// The operand warps' 128 threads: row r's grouped position, slot, scale and rank (position -1:
+// base only), and the distinct slots of the tile in order of first appearance.  The first CTA
+// of the launch reports the segments' and rows' problems, as row_map_kernel does.
+__device__ int4 find_rows(const TileParams &t, TileCtl &ctl, int m0, int r, bool reporter)
 {
-    const int64_t at = (int64_t)row * p.ldy + col;
-    if (p.y_type == 2) {
-        float4 *y = reinterpret_cast<float4 *>(static_cast<float *>(p.Y) + at);
-        y[0] = make_float4(f[0], f[1], f[2], f[3]);
-        y[1] = make_float4(f[4], f[5], f[6], f[7]);
-        return;
-    }
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (p.y_type == 1) {
-            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t *>(&h);
-        } else {
-            w[i] = pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    const int lane = r & 31, warp = r >> 5;
+    ctl.pos[r] = -1;
+    named_sync(kRowBar, 128);
+    if (reporter) {
+        for (int g = r; g < t.n_segments; g += 128) {
+            int rank = 0;
+            float scale = 0.f;
+            const unsigned f = segment_problem(t, g, t.slots[g], t.offsets[g], t.offsets[g + 1], rank, scale);
+            if (f) atomicOr(t.status, f);
         }
     }
-    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.Y) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    // a position counts for its row if its segment is a valid adapter segment
+    int4 info = make_int4(-1, -1, 0, 0);
+    for (int q0 = 0; q0 < t.n_tokens; q0 += 512) {
+        int row[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int q = q0 + 128 * u + r;
+            row[u] = q < t.n_tokens ? (t.token_indices ? t.token_indices[q] : q) : m0 - 1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int q = q0 + 128 * u + r, at = row[u] - m0;
+            const bool in = at >= 0 && at < MR && row[u] < t.n_rows;
+            if (q >= t.n_tokens || (!in && !(reporter && (row[u] < 0 || row[u] >= t.n_rows)))) continue;
+            const int g = segment_of_position(t, q);
+            const int a = t.slots[g], p0 = t.offsets[g], p1 = t.offsets[g + 1];
+            int rank = 0;
+            float scale = 0.f;
+            if (a < 0 || q < p0 || q >= p1 || segment_problem(t, g, a, p0, p1, rank, scale)) continue;
+            if (!in || atomicCAS(&ctl.pos[at], -1, q) != -1) atomicOr(t.status, kFlagBadRow);   // no row, or claimed twice
+        }
+    }
+    named_sync(kRowBar, 128);
+    const int q = ctl.pos[r];
+    if (q >= 0) {
+        const int g = segment_of_position(t, q);
+        int rank = 0;
+        float scale = 0.f;
+        segment_problem(t, g, t.slots[g], t.offsets[g], t.offsets[g + 1], rank, scale);
+        info = make_int4(q, t.slots[g], __float_as_int(scale), rank);
+    }
+    ctl.row_slot[r] = info.y;
+    named_sync(kRowBar, 128);
+    bool first = info.x >= 0;
+    for (int j = 0; j < r && first; ++j)
+        if (ctl.row_slot[j] == info.y) first = false;
+    const unsigned m = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) ctl.part[warp] = __popc(m);
+    named_sync(kRowBar, 128);
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        before += w < warp ? ctl.part[w] : 0;
+        total += ctl.part[w];
+    }
+    if (first) {
+        const int i = before + __popc(m & ((1u << lane) - 1u));
+        ctl.slot[i] = info.y;
+        ctl.bucket[i] = rank_bucket(info.w);
+    }
+    if (r == 0) ctl.count = total;
+    named_sync(kRowBar, 128);
+    return info;
 }
 
 }  // namespace
 
 template <int RK>
-__global__ void __launch_bounds__(MT, 1) mx_gemm_kernel(const __grid_constant__ MxGemmParams p)
+__global__ void __launch_bounds__(MT, 1)
+    mx_tile_kernel(const __grid_constant__ MxGemmParams p, const __grid_constant__ MxSegments sg)
 {
-    using S = Shape<RK>;
+    using S = TileShape<RK>;
     constexpr int GS = S::GS, HOP = S::HOP;
     extern __shared__ __align__(128) uint8_t smem_raw[];
-    __shared__ Ctl ctl;
+    __shared__ TileCtl ctl;
     uint8_t *ring = align_1024(smem_raw);
     uint8_t *hop = ring + GS * STAGE;              // [2][hi, lo]
     uint8_t *zero = hop + 4 * HOP;
@@ -139,22 +239,24 @@ __global__ void __launch_bounds__(MT, 1) mx_gemm_kernel(const __grid_constant__ 
             mbar_init(&ctl.hop_full[b], 1);
             mbar_init(&ctl.hop_empty[b], 1);
         }
+        mbar_init(&ctl.listed, 1);
         fence_mbar_init();
         ctl.fail = 0;
+        ctl.count = 0;
     }
     if (RK > 0) {
-        for (int i = tid; i < S::ZERO / 16; i += MT) reinterpret_cast<uint4 *>(zero)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < (4 * HOP + S::ZERO) / 16; i += MT)
+            reinterpret_cast<uint4 *>(hop)[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    griddep_wait();   // from here on: what earlier kernels wrote
     const uint32_t tmem = ctl.tmem;
     // this CTA's K blocks and adapter slots
     const int nkb = (p.d_in + KB - 1) / KB;
     const int kb0 = nkb * crank / ksplit, kb1 = nkb * (crank + 1) / ksplit;
-    const int32_t *bs = RK ? p.block_slots + (int64_t)mb * kBlockSlotsPitch : nullptr;
-    const int cnt = RK ? bs[0] : 0;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -164,19 +266,21 @@ __global__ void __launch_bounds__(MT, 1) mx_gemm_kernel(const __grid_constant__ 
                 if (g >= GS && !mwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
                 uint8_t *st = ring + s * STAGE;
                 mbar_arrive_expect_tx(&ctl.full[s], STAGE);
-                tma_load_2d(st, &p.x_map, kb * (KB / 2), m0, &ctl.full[s]);
                 tma_load_2d(st + OP_BYTES, &p.w_map, kb * (KB / 2), n0, &ctl.full[s]);
-                bulk_load(st + 2 * OP_BYTES, p.x_scales + ((int64_t)mb * nkb + kb) * SF_BYTES, SF_BYTES, &ctl.full[s]);
-                bulk_load(st + 2 * OP_BYTES + SF_BYTES, p.w_scales + ((int64_t)nb * nkb + kb) * SF_BYTES, SF_BYTES,
-                          &ctl.full[s]);
+                tma_load_2d(st, &p.x_map, kb * (KB / 2), m0, &ctl.full[s]);
+                tma_load_2d(st + 2 * OP_BYTES, &p.xs_map, kb * 256, mb, &ctl.full[s]);
+                tma_load_2d(st + 2 * OP_BYTES + SF_BYTES, &p.ws_map, kb * 256, nb, &ctl.full[s]);
             }
-            for (int j = crank; j < cnt && !ctl.fail; j += ksplit, ++g) {
-                const int slot = bs[1 + 2 * j], R = bs[2 + 2 * j];
-                const int s = (int)(g % GS);
-                if (g >= GS && !mwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
-                // columns past d_out read as zeros
-                mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)R * MC * 2);
-                tma_load_4d(ring + s * STAGE, &p.b_map[bucket_index(R)], 0, n0 / p.b_col_div, 0, slot, &ctl.full[s]);
+            if (RK > 0 && mwait(p, ctl, &ctl.listed, 0)) {
+                const int cnt = ctl.count;
+                for (int j = crank; j < cnt; j += ksplit, ++g) {
+                    const int R = ctl.bucket[j], s = (int)(g % GS);
+                    if (g >= GS && !mwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+                    // columns past d_out read as zeros
+                    mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)R * MC * 2);
+                    tma_load_4d(ring + s * STAGE, &p.b_map[bucket_index(R)], 0, n0 / p.b_col_div, 0, ctl.slot[j],
+                                &ctl.full[s]);
+                }
             }
         }
         __syncwarp();
@@ -194,21 +298,23 @@ __global__ void __launch_bounds__(MT, 1) mx_gemm_kernel(const __grid_constant__ 
                 const uint32_t xs = smem_addr(ring + s * STAGE), ws = xs + OP_BYTES, sf = xs + 2 * OP_BYTES;
                 // the stage's own scale columns: their last readers finished before the stage was refilled
                 const uint32_t sx = tmem + T_SCALES + 16 * s, sw = sx + 8;
-                tmem_copy_scales(sx, sf);
-                tmem_copy_scales(sx + 4, sf + 512);
-                tmem_copy_scales(sw, sf + SF_BYTES);
-                tmem_copy_scales(sw + 4, sf + SF_BYTES + 512);
+                tmem_copy_scales<1>(sx, sf);
+                tmem_copy_scales<1>(sx + 4, sf + 512);
+                tmem_copy_scales<1>(sw, sf + SF_BYTES);
+                tmem_copy_scales<1>(sw + 4, sf + SF_BYTES + 512);
                 const int steps = min(4, (p.d_in - kb * KB + 63) / 64);
                 for (int k = 0; k < steps; ++k)
-                    umma_mxf4(tmem, umma_desc_sw128(xs + 32 * k), umma_desc_sw128(ws + 32 * k),
-                              umma_idesc_mxf4(MR, MC, (k & 1) * 2, (k & 1) * 2), sx + 4 * (k >> 1), sw + 4 * (k >> 1),
-                              kb > kb0 || k > 0 ? 1u : 0u);
+                    umma_mxf4<1>(tmem, umma_desc_sw128(xs + 32 * k), umma_desc_sw128(ws + 32 * k),
+                                 umma_idesc_mxf4(MR, MC, (k & 1) * 2, (k & 1) * 2), sx + 4 * (k >> 1), sw + 4 * (k >> 1),
+                                 kb > kb0 || k > 0 ? 1u : 0u);
                 umma_commit(&ctl.empty[s]);
             }
+            if (RK > 0 && ok) ok = mwait(p, ctl, &ctl.listed, 0);
             if (RK > 0 && ok) {
                 const uint32_t idesc = umma_idesc_bf16(MR, MC);
+                const int cnt = ctl.count;
                 for (int j = crank; j < cnt; j += ksplit, ++g, ++hc) {
-                    const int R = bs[2 + 2 * j];
+                    const int R = ctl.bucket[j];
                     const int s = (int)(g % GS), hb = (int)(hc & 1);
                     if (!mwait(p, ctl, &ctl.hop_full[hb], (hc >> 1) & 1u) || !mwait(p, ctl, &ctl.full[s], (g / GS) & 1u)) {
                         ok = false;
@@ -236,31 +342,26 @@ __global__ void __launch_bounds__(MT, 1) mx_gemm_kernel(const __grid_constant__ 
         __syncwarp();
     } else {
         const int r = tid - 64, quarter = warp & 3;
-        bool alive = true;
+        bool alive = true, lora = false;
         if constexpr (RK > 0) {
-            // operand row r: this row's s H for one slot after the other (zeros for other slots' rows)
-            const int row = m0 + r;
-            int4 info = make_int4(-1, -1, 0, 0);
-            if (cnt > 0 && row < p.n_rows) info = p.row_info[row];
+            const int4 info = find_rows(sg.t, ctl, m0, r, blockIdx.x == 0);
+            if (r == 0) mbar_arrive(&ctl.listed);
+            const int cnt = ctl.count;
+            lora = cnt > crank;   // this CTA has a slot
+            RowOperand<RK> op;
+            if (info.x >= 0) op.load(sg.H + (int64_t)info.x * sg.ldh, info.w, __int_as_float(info.z));
+            bool dirty0 = false, dirty1 = false;   // this row of the buffer holds values
             uint32_t hc = 0;
             for (int j = crank; j < cnt; j += ksplit, ++hc) {
-                const int slot = bs[1 + 2 * j], R = bs[2 + 2 * j], hb = (int)(hc & 1);
+                const int hb = (int)(hc & 1);
                 if (hc >= 2 && !named_sync_and(kRowBar, 128, mwait(p, ctl, &ctl.hop_empty[hb], ((hc >> 1) - 1) & 1u))) {
                     alive = false;
                     break;
                 }
-                const bool mine = info.x >= 0 && info.y == slot;
-                const int rank = mine ? info.w : 0;
-                const float sc = mine ? __int_as_float(info.z) : 0.f;
-                const float *hsrc = p.H + (int64_t)(mine ? info.x : 0) * p.ldh;
-                uint8_t *hi = hop + hb * 2 * HOP;
-                if constexpr (RK == 16) {
-                    stage_operand<16>(hi, hi + HOP, hsrc, rank, sc, r);
-                } else {
-                    if (R <= 16) stage_operand<16>(hi, hi + HOP, hsrc, rank, sc, r);
-                    else if (R == 32) stage_operand<32>(hi, hi + HOP, hsrc, rank, sc, r);
-                    else stage_operand<64>(hi, hi + HOP, hsrc, rank, sc, r);
-                }
+                const bool mine = info.x >= 0 && info.y == ctl.slot[j];
+                if (mine || (hb ? dirty1 : dirty0)) op.store(hop + hb * 2 * HOP, r, mine);
+                if (hb) dirty1 = mine;
+                else dirty0 = mine;
                 fence_proxy_async_smem();
                 named_sync(kRowBar, 128);
                 if (r == 0) mbar_arrive(&ctl.hop_full[hb]);
@@ -271,9 +372,9 @@ __global__ void __launch_bounds__(MT, 1) mx_gemm_kernel(const __grid_constant__ 
             tc_fence_after();
             const int row = m0 + 32 * quarter + lane;
             const uint32_t tb = tmem + ((uint32_t)(32 * quarter) << 16);
-            const bool lora = RK > 0 && cnt > crank;   // this CTA had a slot
             float *red = reinterpret_cast<float *>(ring) + (32 * quarter + lane) * RED_PITCH;
-            for (int c = 0; c < MC; c += 32) {
+            const bool any = m0 + 32 * quarter < p.n_rows;   // a row of this warp exists
+            for (int c = 0; c < MC && any; c += 32) {
                 uint32_t v[32];
                 tmem_ld32(tb + c, v);
                 tmem_wait_ld();
@@ -337,63 +438,498 @@ __global__ void __launch_bounds__(MT, 1) mx_gemm_kernel(const __grid_constant__ 
     if (warp == 1) tmem_dealloc(tmem, T_COLS);
 }
 
+// ------------------------------------------------------------------ many rows
+// Persistent 256 x 256 tiles on pairs of CTAs (a cluster of two on neighbouring SMs) with
+// tcgen05.mma.cta_group::2: CTA c holds rows [128 c, +128) of the tile's X and of its W columns,
+// and 128 rows of the fp32 accumulator (256 columns of tensor memory; the rest holds the stages'
+// scales, so there is no room for a second accumulator).  The epilogue therefore takes the tile
+// out of tensor memory in one go, as 16-bit values in the registers of eight warps, hands the
+// accumulator back and stores while the next tile's products run.
+//   warp 0     TMA of both CTAs onto the even one's barriers, as in base_gemm.cu: per K block the
+//              CTA's codes of X and half of W's, its rows' scales of X and all 256 columns' of W
+//   warp 1     even CTA: the products of the pair; after the K blocks it waits for them before the
+//              low-rank products, whose instruction kind differs, continue the same accumulator
+//   warps 2-5  offer the rows' s H slot by slot
+//   warps 6-13 epilogue: quarter = warp % 4 of the rows, half = (warp - 6) / 4 of the columns
 namespace {
 
-template <int RK>
-cudaError_t launch_tile(const MxGemmParams &p, int ksplit, cudaStream_t stream)
-{
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)(p.n_mblk * p.n_nblk * ksplit), 1, 1);
-    cfg.blockDim = dim3(MT, 1, 1);
-    cfg.dynamicSmemBytes = Shape<RK>::SMEM;
-    cfg.stream = stream;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)ksplit;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, mx_gemm_kernel<RK>, p);
-}
+constexpr int PN = 256;                    // columns per tile
+constexpr int PH = 128;                    // W rows (and B columns) per CTA
+constexpr int P_STAGE = 2 * OP_BYTES + 3 * SF_BYTES + 1024;   // a multiple of 1 KB, as the swizzle wants
+constexpr int PT = 14 * 32;
+constexpr int P_SCALES = 256, P_COLS = 512;
+constexpr int P_SF_COLS = 24;              // 8 for X, 16 for W per stage
+constexpr uint16_t kPairMask = 0x3;
+constexpr int kGroupRows = 8;              // row blocks per group of tiles (see tile_at)
 
 template <int RK>
-cudaError_t prepare_tile()
+struct PairShape {
+    static constexpr int HOP = MR * RK * 2;
+    static constexpr int HB = RK == 64 ? 1 : 2;        // operand buffers
+    static constexpr int GS = RK ? 5 : 6;               // ring stages
+    static constexpr int ZERO = RK ? 2048 : 0;
+    static constexpr int SMEM = 1024 + GS * P_STAGE + HB * 2 * HOP + ZERO;
+    static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
+    static_assert(P_SCALES + P_SF_COLS * GS <= P_COLS, "tensor memory");
+    static_assert(P_STAGE % 1024 == 0 && PH * RK * 2 <= P_STAGE, "stage layout");
+};
+
+struct PairCtl {
+    uint64_t full[6], empty[6];
+    uint64_t acc_full, acc_empty;
+    uint64_t k_done;               // the K blocks' products are complete
+    uint64_t hop_full[2], hop_empty[2];
+    uint32_t tmem;
+    volatile int fail;
+};
+
+// On expiry both CTAs of the pair are told to stop.
+__device__ __forceinline__ bool pwait(const MxGemmParams &p, PairCtl &ctl, uint64_t *bar, uint32_t parity)
 {
-    cudaError_t e = cudaFuncSetAttribute(mx_gemm_kernel<RK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<RK>::SMEM);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(mx_gemm_kernel<RK>, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+    if (ctl.fail) return false;
+    if (!mbar_wait_bounded_cluster(bar, parity, kMxWaitNs)) {
+        ctl.fail = 1;
+        st_cluster_u32(map_to_rank(smem_addr((const void *)&ctl.fail), cluster_rank() ^ 1u), 1u);
+        atomicOr(p.status, kFlagTimeout);
+        return false;
+    }
+    return true;
+}
+
+// Tiles run in groups of kGroupRows row blocks, column-major inside a group, so that the pairs
+// working at the same time share a few row blocks of X and column blocks of W in L2.
+__device__ __forceinline__ void tile_at(const MxGemmParams &p, int t, int &mb, int &nb)
+{
+    const int per_group = kGroupRows * p.n_nblk;
+    const int first_mb = (t / per_group) * kGroupRows;
+    const int rows = min(kGroupRows, p.n_mblk - first_mb);
+    const int local = t % per_group;
+    mb = first_mb + local % rows;
+    nb = local / rows;
+}
+
+__device__ __forceinline__ uint32_t leader_bar(const uint64_t *bar) { return map_to_rank(smem_addr(bar), 0); }
+
+// 8 x 8 transpose of 16-byte pieces across groups of eight lanes: lane k of a group ends up with
+// piece k of the group's eight rows, so that a store instruction writes whole 128-byte lines.
+__device__ __forceinline__ void transpose8(uint4 (&a)[8], int k)
+{
+#pragma unroll
+    for (int sh = 4; sh >= 1; sh >>= 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j & sh) continue;
+            const bool upper = (k & sh) != 0;
+            const uint4 send = upper ? a[j] : a[j | sh];
+            uint4 recv;
+            recv.x = __shfl_xor_sync(0xffffffffu, send.x, sh);
+            recv.y = __shfl_xor_sync(0xffffffffu, send.y, sh);
+            recv.z = __shfl_xor_sync(0xffffffffu, send.z, sh);
+            recv.w = __shfl_xor_sync(0xffffffffu, send.w, sh);
+            if (upper) a[j] = recv;
+            else a[j | sh] = recv;
+        }
+    }
 }
 
 }  // namespace
 
-cudaError_t launch_mx_gemm(const MxGemmParams &p, int rank_bucket_max, cudaStream_t stream)
+// YT: 0 bf16, 1 fp16, 2 fp32 (an fp32 tile does not fit the epilogue's registers: it is stored
+// from tensor memory chunk by chunk, and the accumulator handed back after the last).
+template <int RK, int YT>
+__global__ void __launch_bounds__(PT, 1)
+    mx_pair_kernel(const __grid_constant__ MxGemmParams p, const __grid_constant__ MxSlots sl)
 {
-    // CTAs per tile: waves of resident CTAs (one per SM) times K blocks per CTA, plus what a
-    // part costs beside its K blocks.
+    using S = PairShape<RK>;
+    constexpr int GS = S::GS, HOP = S::HOP, HB = S::HB;
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    __shared__ PairCtl ctl;
+    uint8_t *ring = align_1024(smem_raw);
+    uint8_t *hop = ring + GS * P_STAGE;            // [HB][hi, lo]
+    uint8_t *zero = hop + HB * 2 * HOP;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int crank = (int)cluster_rank();         // 0 issues the pair's products
+    const bool leader = crank == 0;
+    const int n_clusters = (int)(gridDim.x / 2), first = (int)cluster_index();
+
+    if (warp == 1) {
+        tmem_alloc_pair(&ctl.tmem, P_COLS);
+        tmem_relinquish_pair();
+    }
+    if (tid == 0) {
+        for (int s = 0; s < GS; ++s) {
+            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.empty[s], 1);
+        }
+        mbar_init(&ctl.acc_full, 1);
+        mbar_init(&ctl.acc_empty, 16);             // eight epilogue warps in each CTA
+        mbar_init(&ctl.k_done, 1);
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&ctl.hop_full[b], 2);        // one arrival per CTA
+            mbar_init(&ctl.hop_empty[b], 1);
+        }
+        fence_mbar_init();
+        ctl.fail = 0;
+    }
+    if (RK > 0) {
+        for (int i = tid; i < (HB * 2 * HOP + S::ZERO) / 16; i += PT)
+            reinterpret_cast<uint4 *>(hop)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive_release();   // both CTAs' barriers exist before either signals the other's
+    cluster_wait_acquire();
+    tc_fence_after();
+    griddep_wait();
+    const uint32_t tmem = ctl.tmem;
+    const int n_tiles = p.n_mblk * p.n_nblk;
     const int nkb = (p.d_in + KB - 1) / KB;
-    const int64_t tiles = (int64_t)p.n_mblk * p.n_nblk;
-    int best = 1;
-    int64_t best_cost = INT64_MAX;
-    for (int ks = 1; ks <= 8 && ks <= nkb; ks *= 2) {
-        const int64_t waves = (tiles * ks + 147) / 148;
-        const int64_t cost = waves * ((nkb + ks - 1) / ks + 4) + (ks > 1 ? 2 : 0);
-        if (cost < best_cost) {
-            best_cost = cost;
-            best = ks;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t g = 0;
+            for (int t = first; t < n_tiles && !ctl.fail; t += n_clusters) {
+                int mb, nb;
+                tile_at(p, t, mb, nb);
+                const int m0 = (2 * mb + crank) * MR, nc = nb * PN + PH * crank;
+                for (int kb = 0; kb < nkb; ++kb, ++g) {
+                    const int s = (int)(g % GS);
+                    if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+                    uint8_t *st = ring + s * P_STAGE;
+                    if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * (2 * OP_BYTES + 3 * SF_BYTES));
+                    const uint32_t fb = leader_bar(&ctl.full[s]);
+                    // rows past the end, and their scales, read as zeros
+                    tma_load_2d_pair(st, &p.x_map, kb * (KB / 2), m0, fb);
+                    tma_load_2d_pair(st + OP_BYTES, &p.w_map, kb * (KB / 2), nc, fb);
+                    tma_load_2d_pair(st + 2 * OP_BYTES, &p.xs_map, kb * 256, 2 * mb + crank, fb);
+                    tma_load_2d_pair(st + 2 * OP_BYTES + SF_BYTES, &p.ws_map, kb * 256, 2 * nb, fb);
+                    tma_load_2d_pair(st + 2 * OP_BYTES + 2 * SF_BYTES, &p.ws_map, kb * 256, 2 * nb + 1, fb);
+                }
+                if constexpr (RK > 0) {
+                    const int32_t *bs = sl.block_slots + (int64_t)mb * kBlockSlotsPitch;
+                    const int cnt = bs[0];
+                    for (int j = 0; j < cnt && !ctl.fail; ++j, ++g) {
+                        const int slot = bs[1 + 2 * j], R = bs[2 + 2 * j], s = (int)(g % GS);
+                        if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+                        if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * (uint32_t)R * PH * 2);
+                        tma_load_4d_pair(ring + s * P_STAGE, &p.b_map[bucket_index(R)], 0, nc / p.b_col_div, 0, slot,
+                                         leader_bar(&ctl.full[s]));
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (leader && lane == 0) {
+            uint32_t g = 0, hc = 0, tc = 0, kc = 0;
+            bool ok = true;
+            for (int t = first; t < n_tiles && ok; t += n_clusters, ++tc) {
+                int mb, nb;
+                tile_at(p, t, mb, nb);
+                for (int kb = 0; kb < nkb && ok; ++kb, ++g) {
+                    const int s = (int)(g % GS);
+                    if (!pwait(p, ctl, &ctl.full[s], (g / GS) & 1u) ||
+                        (kb == 0 && tc > 0 && !pwait(p, ctl, &ctl.acc_empty, (tc - 1) & 1u))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t xs = smem_addr(ring + s * P_STAGE), ws = xs + OP_BYTES, sf = xs + 2 * OP_BYTES;
+                    const uint32_t sx = tmem + P_SCALES + P_SF_COLS * s, sw = sx + 8;
+                    // per 128 of K: X's four columns; W's eight, for columns 0-127 and 128-255
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        tmem_copy_scales<2>(sx + 4 * h, sf + 512 * h);
+                        tmem_copy_scales<2>(sw + 8 * h, sf + SF_BYTES + 512 * h);
+                        tmem_copy_scales<2>(sw + 8 * h + 4, sf + 2 * SF_BYTES + 512 * h);
+                    }
+                    const int steps = min(4, (p.d_in - kb * KB + 63) / 64);
+                    for (int k = 0; k < steps; ++k)
+                        umma_mxf4<2>(tmem, umma_desc_sw128(xs + 32 * k), umma_desc_sw128(ws + 32 * k),
+                                     umma_idesc_mxf4(2 * MR, PN, (k & 1) * 2, (k & 1) * 2), sx + 4 * (k >> 1),
+                                     sw + 8 * (k >> 1), kb > 0 || k > 0 ? 1u : 0u);
+                    umma_commit_pair(&ctl.empty[s], kPairMask);
+                }
+                if constexpr (RK > 0) {
+                    const int32_t *bs = sl.block_slots + (int64_t)mb * kBlockSlotsPitch;
+                    const int cnt = ok ? bs[0] : 0;
+                    if (cnt > 0) {
+                        umma_commit_pair(&ctl.k_done, kPairMask);
+                        ok = pwait(p, ctl, &ctl.k_done, kc++ & 1u);
+                    }
+                    const uint32_t idesc = umma_idesc_bf16(2 * MR, PN);
+                    for (int j = 0; j < cnt && ok; ++j, ++g, ++hc) {
+                        const int R = bs[2 + 2 * j], s = (int)(g % GS), hb = (int)(hc % HB);
+                        if (!pwait(p, ctl, &ctl.hop_full[hb], (hc / HB) & 1u) ||
+                            !pwait(p, ctl, &ctl.full[s], (g / GS) & 1u)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t a_hi = smem_addr(hop + hb * 2 * HOP), a_lo = a_hi + HOP;
+                        const uint32_t b_s = smem_addr(ring + s * P_STAGE);
+                        for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
+                            const uint32_t b0 = b_s + st * 2 * PH * 16;
+                            const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PH * 16;
+                            const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
+                            const uint32_t koff = st * 2 * (MR / 8) * 128;
+                            umma_bf16_pair(tmem, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd, idesc, 1u);
+                            umma_bf16_pair(tmem, umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd, idesc, 1u);
+                        }
+                        umma_commit_pair(&ctl.empty[s], kPairMask);
+                        umma_commit_pair(&ctl.hop_empty[hb], kPairMask);
+                    }
+                }
+                if (ok) umma_commit_pair(&ctl.acc_full, kPairMask);
+            }
+        }
+        __syncwarp();
+    } else if (warp < 6) {
+        if constexpr (RK > 0) {
+            const int r = tid - 64;
+            const uint32_t full0 = leader_bar(&ctl.hop_full[0]), full1 = leader_bar(&ctl.hop_full[1]);
+            uint32_t hc = 0;
+            bool alive = true, dirty0 = false, dirty1 = false;
+            for (int t = first; t < n_tiles && alive; t += n_clusters) {
+                int mb, nb;
+                tile_at(p, t, mb, nb);
+                const int32_t *bs = sl.block_slots + (int64_t)mb * kBlockSlotsPitch;
+                const int cnt = bs[0];
+                if (cnt == 0) continue;
+                const int row = (2 * mb + crank) * MR + r;
+                int4 info = make_int4(-1, -1, 0, 0);
+                if (row < p.n_rows) info = sl.row_info[row];
+                RowOperand<RK> op;
+                if (info.x >= 0) op.load(sl.H + (int64_t)info.x * sl.ldh, info.w, __int_as_float(info.z));
+                for (int j = 0; j < cnt; ++j, ++hc) {
+                    const int hb = (int)(hc % HB);
+                    if (hc >= HB && !named_sync_and(kRowBar, 128, pwait(p, ctl, &ctl.hop_empty[hb], ((hc / HB) - 1) & 1u))) {
+                        alive = false;
+                        break;
+                    }
+                    const bool mine = info.x >= 0 && info.y == bs[1 + 2 * j];
+                    if (mine || (hb ? dirty1 : dirty0)) op.store(hop + hb * 2 * HOP, r, mine);
+                    if (hb) dirty1 = mine;
+                    else dirty0 = mine;
+                    fence_proxy_async_smem();
+                    named_sync(kRowBar, 128);
+                    if (r == 0) mbar_arrive_cluster(hb ? full1 : full0);
+                }
+            }
+        }
+    } else {
+        const int quarter = warp & 3, half = (warp - 6) >> 2;
+        const uint32_t empty_bar = leader_bar(&ctl.acc_empty);
+        const int k = lane & 7;
+        uint32_t tc = 0;
+        for (int t = first; t < n_tiles; t += n_clusters, ++tc) {
+            int mb, nb;
+            tile_at(p, t, mb, nb);
+            if (!named_sync_and(kEpiBar, 256, pwait(p, ctl, &ctl.acc_full, tc & 1u))) break;
+            tc_fence_after();
+            const int n0 = nb * PN + 128 * half;
+            const int warp_row = (2 * mb + crank) * MR + 32 * quarter;
+            const uint32_t tb = tmem + ((uint32_t)(32 * quarter) << 16) + 128 * half;
+            if constexpr (YT == 2) {
+                const int row = warp_row + lane;
+                for (int c = 0; c < 128; c += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(tb + c, v);
+                    tmem_wait_ld();
+                    if (c == 96) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(empty_bar);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * q + i]);
+                        if (row < p.n_rows && n0 + c + 8 * q < p.d_out) store8<2>(p, row, n0 + c + 8 * q, f);
+                    }
+                }
+            } else {
+                uint4 a[2][8];   // this lane's row, 128 columns
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    tmem_ld32(tb + 32 * c, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = pack2<YT>(__uint_as_float(v[8 * q + 2 * i]), __uint_as_float(v[8 * q + 2 * i + 1]));
+                        a[c >> 1][(c & 1) * 4 + q] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(empty_bar);
+                const int row0 = warp_row + 8 * (lane >> 3);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    transpose8(a[h], k);
+                    const int col = n0 + 64 * h + 8 * k;
+                    if (col < p.d_out) {   // d_out is a multiple of 8
+                        uint16_t *y = static_cast<uint16_t *>(p.Y) + col;
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (row0 + j < p.n_rows) *reinterpret_cast<uint4 *>(y + (int64_t)(row0 + j) * p.ldy) = a[h][j];
+                    }
+                }
+            }
         }
     }
-    if (rank_bucket_max == 0) return launch_tile<0>(p, best, stream);
-    if (rank_bucket_max <= 16) return launch_tile<16>(p, best, stream);
-    return launch_tile<64>(p, best, stream);
+
+    // leave: tensor-core work done, copies landed, neither CTA still signals the other
+    __syncthreads();
+    if (ctl.fail && tid == 0) {
+        const uint64_t t0 = global_timer_ns();
+        while (global_timer_ns() - t0 < 2000000ull) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_arrive_release();
+    cluster_wait_acquire();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc_pair(tmem, P_COLS);
+}
+
+// ------------------------------------------------------------------ launches
+namespace {
+
+cudaLaunchConfig_t config(unsigned ctas, unsigned threads, size_t smem, unsigned cluster, cudaStream_t stream,
+                          cudaLaunchAttribute (&attr)[2])
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ctas, 1, 1);
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cfg;
+}
+
+template <int RK>
+cudaError_t launch_tile(const MxGemmParams &p, const MxSegments &sg, int ksplit, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg =
+        config((unsigned)(p.n_mblk * p.n_nblk * ksplit), MT, TileShape<RK>::SMEM, (unsigned)ksplit, stream, attr);
+    return cudaLaunchKernelEx(&cfg, mx_tile_kernel<RK>, p, sg);
+}
+
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes)
+{
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
+}
+
+template <int RK>
+cudaError_t prepare_rank()
+{
+    cudaError_t e;
+    if ((e = allow_smem(mx_tile_kernel<RK>, TileShape<RK>::SMEM)) != cudaSuccess) return e;
+    if ((e = allow_smem(mx_pair_kernel<RK, 0>, PairShape<RK>::SMEM)) != cudaSuccess) return e;
+    if ((e = allow_smem(mx_pair_kernel<RK, 1>, PairShape<RK>::SMEM)) != cudaSuccess) return e;
+    return allow_smem(mx_pair_kernel<RK, 2>, PairShape<RK>::SMEM);
+}
+
+// Pairs resident at once on the current device (cached per device; every variant takes whole SMs).
+cudaError_t active_pairs(int &active)
+{
+    static std::mutex mu;
+    static int cached[64] = {};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (cached[dev] == 0) {
+        cudaLaunchAttribute attr[2];
+        cudaLaunchConfig_t cfg = config(2, PT, PairShape<0>::SMEM, 2, nullptr, attr);
+        cfg.numAttrs = 1;
+        int n = 0;
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<0, 0>, &cfg);
+        if (e != cudaSuccess) return e;
+        if (n <= 0) return cudaErrorInvalidConfiguration;
+        cached[dev] = n;
+    }
+    active = cached[dev];
+    return cudaSuccess;
+}
+
+template <int RK>
+cudaError_t launch_pair(const MxGemmParams &p, const MxSlots &sl, unsigned pairs, cudaStream_t stream)
+{
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = config(2 * pairs, PT, PairShape<RK>::SMEM, 2, stream, attr);
+    if (p.y_type == 0) return cudaLaunchKernelEx(&cfg, mx_pair_kernel<RK, 0>, p, sl);
+    if (p.y_type == 1) return cudaLaunchKernelEx(&cfg, mx_pair_kernel<RK, 1>, p, sl);
+    return cudaLaunchKernelEx(&cfg, mx_pair_kernel<RK, 2>, p, sl);
+}
+
+}  // namespace
+
+MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
+{
+    // Time of each form in units of one K block of a 128 x 128 tile on one SM: waves of
+    // resident CTAs times (K blocks per CTA + what a tile costs beside them).  A pair tile's K
+    // block is two of those units of tensor-core work per SM.
+    const int64_t nkb = (d_in + KB - 1) / KB;
+    const int64_t tiles = (int64_t)((n_rows + 127) / 128) * ((d_out + MC - 1) / MC);
+    MxPlan plan{1, 1};
+    int64_t best = INT64_MAX;
+    for (int ks = 1; ks <= 8 && ks <= nkb; ks *= 2) {
+        const int64_t cost = (tiles * ks + 147) / 148 * ((nkb + ks - 1) / ks + 4) + (ks > 1 ? 2 : 0);
+        if (cost < best) {
+            best = cost;
+            plan.ksplit = ks;
+        }
+    }
+    const int64_t pairs = (int64_t)((n_rows + 255) / 256) * ((d_out + PN - 1) / PN);
+    const int64_t pair_cost = (pairs + 73) / 74 * (2 * nkb + 2) + 6;
+    plan.tile = pair_cost < best ? 0 : 1;
+    return plan;
+}
+
+cudaError_t launch_mx_tile(const MxGemmParams &p, const MxSegments &sg, int rank_bucket_max, int ksplit,
+                           cudaStream_t stream)
+{
+    if (rank_bucket_max == 0) return launch_tile<0>(p, sg, ksplit, stream);
+    if (rank_bucket_max <= 16) return launch_tile<16>(p, sg, ksplit, stream);
+    return launch_tile<64>(p, sg, ksplit, stream);
+}
+
+cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int rank_bucket_max, cudaStream_t stream)
+{
+    int active = 0;
+    cudaError_t e = active_pairs(active);
+    if (e != cudaSuccess) return e;
+    const unsigned pairs = (unsigned)std::min<int64_t>((int64_t)p.n_mblk * p.n_nblk, active);
+    if (rank_bucket_max == 0) return launch_pair<0>(p, sl, pairs, stream);
+    if (rank_bucket_max <= 16) return launch_pair<16>(p, sl, pairs, stream);
+    return launch_pair<64>(p, sl, pairs, stream);
 }
 
 cudaError_t prepare_mx_gemm()
 {
     cudaError_t e;
-    if ((e = prepare_tile<0>()) != cudaSuccess) return e;
-    if ((e = prepare_tile<16>()) != cudaSuccess) return e;
-    return prepare_tile<64>();
+    if ((e = prepare_rank<0>()) != cudaSuccess) return e;
+    if ((e = prepare_rank<16>()) != cudaSuccess) return e;
+    return prepare_rank<64>();
 }
 
 }  // namespace mlora

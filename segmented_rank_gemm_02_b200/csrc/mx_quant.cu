@@ -129,6 +129,7 @@ __device__ __forceinline__ uint8_t *scale_vec(const MxRows &q, int row0, int chu
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) mx_quantize_kernel(const T *X, int64_t ldx, const MxRows q)
 {
+    griddep_launch_dependents();   // a product of Q may set itself up meanwhile; it waits for this grid
     const int lane = threadIdx.x & 31;
     int row0, chunk;
     if (!my_unit(q, ((int64_t)blockIdx.x * kQuantThreads + threadIdx.x) >> 5, row0, chunk)) return;

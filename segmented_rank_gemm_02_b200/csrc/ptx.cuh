@@ -723,23 +723,28 @@ __host__ __device__ constexpr uint32_t umma_idesc_mxf4(int m, int n, int sfa, in
 }
 
 // D[tmem] (+)= (A scaled) (B scaled)^T, operands in shared memory, scales in tensor memory.
+// G = 2: over a pair of CTAs, issued by the even one (M = 256; each CTA's tensor memory holds the
+// scales of its own rows of A and of all of B).
+template <int G>
 __device__ __forceinline__ void umma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                           uint32_t sfa_tmem, uint32_t sfb_tmem, uint32_t accumulate)
 {
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n"
-        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        "tcgen05.mma.cta_group::%7.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n"
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate), "n"(G)
         : "memory");
 }
 
 // 32 rows x 16 bytes of shared memory (rows 16 bytes apart) to four tensor-memory columns,
-// row i to lane i of all four lane quarters: one 512-byte tile of scales.
+// row i to lane i of all four lane quarters: one 512-byte tile of scales.  G = 2: each CTA
+// of the pair from its own shared memory to its own tensor memory.
+template <int G>
 __device__ __forceinline__ void tmem_copy_scales(uint32_t taddr, uint32_t smem_byte_addr)
 {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;"
-                 ::"r"(taddr), "l"(umma_desc_kmajor(smem_byte_addr, 128, 128))
+    asm volatile("tcgen05.cp.cta_group::%2.32x128b.warpx4 [%0], %1;"
+                 ::"r"(taddr), "l"(umma_desc_kmajor(smem_byte_addr, 128, 128)), "n"(G)
                  : "memory");
 }
 

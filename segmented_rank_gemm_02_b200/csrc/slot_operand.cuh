@@ -2,6 +2,7 @@
 // tensor core (base_gemm.cu, mx_gemm.cu).
 #pragma once
 
+#include "kernels.cuh"
 #include "ptx.cuh"
 
 namespace mlora {
@@ -48,6 +49,80 @@ __device__ __forceinline__ void stage_operand(uint8_t *hi, uint8_t *lo, const fl
         *reinterpret_cast<uint4 *>(hi + off) = vh;
         *reinterpret_cast<uint4 *>(lo + off) = vl;
     }
+}
+
+// One row's s * H in registers, as the bf16 hi + lo parts that stage_operand writes, for kernels
+// that offer the operand slot by slot: a row belongs to one slot, so its values are loaded once
+// and written once, and the buffers are zero everywhere else.
+template <int RK>
+struct RowOperand {
+    uint32_t hi[RK / 2], lo[RK / 2];
+
+    __device__ __forceinline__ void load(const float *hsrc, int rank, float sc)
+    {
+        float h[RK];
+        if (rank == RK) {
+#pragma unroll
+            for (int i = 0; i < RK / 4; ++i) {
+                const float4 v = reinterpret_cast<const float4 *>(hsrc)[i];
+                h[4 * i] = v.x, h[4 * i + 1] = v.y, h[4 * i + 2] = v.z, h[4 * i + 3] = v.w;
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < RK; ++c) h[c] = c < rank ? hsrc[c] : 0.f;
+        }
+#pragma unroll
+        for (int c = 0; c < RK / 2; ++c) {
+            float h0, l0, h1, l1;
+            split_bf16(sc * h[2 * c], h0, l0);
+            split_bf16(sc * h[2 * c + 1], h1, l1);
+            hi[c] = pack_bf16x2(h0, h1);
+            lo[c] = pack_bf16x2(l0, l1);
+        }
+    }
+
+    // Row r of a buffer (hi, then lo): the values, or zeros.
+    __device__ __forceinline__ void store(uint8_t *buf, int r, bool values) const
+    {
+        constexpr int HOP = kOperandRows * RK * 2;
+#pragma unroll
+        for (int cg = 0; cg < RK / 8; ++cg) {
+            const int off = (cg * (kOperandRows / 8) + r / 8) * 128 + (r % 8) * 16;
+            const uint4 z = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4 *>(buf + off) =
+                values ? make_uint4(hi[4 * cg], hi[4 * cg + 1], hi[4 * cg + 2], hi[4 * cg + 3]) : z;
+            *reinterpret_cast<uint4 *>(buf + HOP + off) =
+                values ? make_uint4(lo[4 * cg], lo[4 * cg + 1], lo[4 * cg + 2], lo[4 * cg + 3]) : z;
+        }
+    }
+};
+
+// The problems of segment g (status bits as the other kernels report them), 0 if it
+// is a valid adapter segment; *rank and *scale are set for a valid one.
+__device__ __forceinline__ unsigned segment_problem(const TileParams &p, int g, int a, int p0, int p1, int &rank,
+                                                    float &scale)
+{
+    if (a < -1 || a >= p.n_slots) return kFlagBadSlot;
+    if (p0 < 0 || p1 < p0 || p1 > p.n_tokens) return kFlagBadOffsets;
+    if (a < 0) return 0;
+    rank = p.slot_rank[a];
+    scale = p.scales ? p.scales[g] : p.slot_scale[a];
+    if (p.generations && p.slot_gen[a] != p.generations[g]) return kFlagStaleSlot;
+    if (rank <= 0) return kFlagSlotEmpty;
+    if ((p.ranks && p.ranks[g] != rank) || rank_bucket(rank) == 0) return kFlagBadRank;
+    return 0;
+}
+
+// The segment that may hold grouped position q: the last g with offsets[g] <= q.
+__device__ __forceinline__ int segment_of_position(const TileParams &p, int q)
+{
+    int lo = 0, hi = p.n_segments - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (p.offsets[mid] <= q) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
 }
 
 }  // namespace mlora
