@@ -213,6 +213,72 @@ __global__ void __launch_bounds__(PM) block_slots_kernel(const int4 *row_info, i
     if (tid == 0) o[0] = total;
 }
 
+// The two kernels above and the memset before them in one launch: every block looks through
+// the whole list of grouped positions for its 256 rows (512 threads, from L2), which is quicker
+// than two more launches as long as the list is short.
+constexpr int kSearchThreads = 512;
+
+__global__ void __launch_bounds__(kSearchThreads)
+    row_blocks_kernel(const __grid_constant__ TileParams p, int4 *row_info, int32_t *block_slots)
+{
+    __shared__ int s_pos[PM];
+    __shared__ __align__(16) int s_slot[PM];
+    __shared__ int s_count[PM / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row0 = blockIdx.x * PM;
+    const bool reporter = blockIdx.x == 0;
+    if (tid < PM) s_pos[tid] = -1;
+    __syncthreads();
+    if (reporter) {
+        for (int g = tid; g < p.n_segments; g += kSearchThreads) {
+            int rank = 0;
+            float scale = 0.f;
+            const unsigned f = segment_problem(p, g, p.slots[g], p.offsets[g], p.offsets[g + 1], rank, scale);
+            if (f) atomicOr(p.status, f);
+        }
+    }
+    for (int64_t q0 = tid; q0 < p.n_tokens; q0 += 4 * kSearchThreads) {
+        int row[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t q = q0 + u * kSearchThreads;
+            row[u] = q < p.n_tokens && p.token_indices ? p.token_indices[q] : (int)q;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t q = q0 + u * kSearchThreads;
+            const int at = q < p.n_tokens ? claimed_row(p, (int)q, row[u], row0, PM, reporter) : -1;
+            if (at >= 0 && atomicCAS(&s_pos[at], -1, (int)q) != -1) atomicOr(p.status, kFlagBadRow);
+        }
+    }
+    __syncthreads();
+    int4 info = make_int4(-1, -1, 0, 0);
+    if (tid < PM) {
+        if (s_pos[tid] >= 0) info = row_of_position(p, s_pos[tid]);
+        if (row0 + tid < p.n_rows) row_info[row0 + tid] = info;
+        s_slot[tid] = info.y;
+    }
+    __syncthreads();
+    if (tid >= PM) return;
+    const bool first = first_with_slot(s_slot, tid, info.y);
+    const unsigned m = __ballot_sync(0xffffffffu, first);
+    if (lane == 0) s_count[warp] = __popc(m);
+    named_sync(1, PM);
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < PM / 32; ++w) {
+        before += w < warp ? s_count[w] : 0;
+        total += s_count[w];
+    }
+    int32_t *o = block_slots + (int64_t)blockIdx.x * kBlockSlotsPitch;
+    if (first) {
+        const int idx = before + __popc(m & ((1u << lane) - 1u));
+        o[1 + 2 * idx] = info.y;
+        o[2 + 2 * idx] = rank_bucket(info.w);
+    }
+    if (tid == 0) o[0] = total;
+}
+
 // ------------------------------------------------------------------ GEMM
 // Pair tiles t = cluster index, + number of clusters, ...; tile t covers rows
 // [256 mb, +256) and columns [GN nb, +GN) with (mb, nb) from tile_coords.  Every role
@@ -543,6 +609,21 @@ cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_
     if (n_mblk <= 0) return cudaSuccess;
     block_slots_kernel<<<n_mblk, PM, 0, stream>>>(row_info, n_rows, block_slots);
     return cudaGetLastError();
+}
+
+// Up to this many grouped positions every row block searches the list itself.
+constexpr int kSearchTokens = 32768;
+
+cudaError_t launch_row_blocks(const TileParams &p, int4 *row_info, int32_t *block_slots, cudaStream_t stream)
+{
+    const int n_mblk = (p.n_rows + PM - 1) / PM;
+    if (n_mblk <= 0) return cudaSuccess;
+    if (p.n_segments > 0 && p.n_tokens <= kSearchTokens) {
+        row_blocks_kernel<<<n_mblk, kSearchThreads, 0, stream>>>(p, row_info, block_slots);
+        return cudaGetLastError();
+    }
+    const cudaError_t e = launch_row_map(p, row_info, stream);
+    return e != cudaSuccess ? e : launch_block_slots(row_info, p.n_rows, block_slots, stream);
 }
 
 namespace {

@@ -208,6 +208,8 @@ struct GemmParams {
 cudaError_t launch_row_map(const TileParams &p, int4 *row_info, cudaStream_t stream);
 // The distinct slots of each 256-row block of rows.
 cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream);
+// Both, in one launch where the list of grouped positions is short.
+cudaError_t launch_row_blocks(const TileParams &p, int4 *row_info, int32_t *block_slots, cudaStream_t stream);
 // Tile width (256 or 512 columns of Y) for n_mblk 256-row blocks and d_out columns.
 int choose_gemm_cols(int n_mblk, int d_out);
 // Persistent GEMM over all (256-row, gn-column) tiles, one pair of CTAs per two SMs;
@@ -222,8 +224,10 @@ constexpr int kMxTileRows = 128;   // rows of Y per CTA
 
 // What every launch of the 4-bit GEMM needs.  Passed by value.
 struct MxGemmParams {
-    CUtensorMap x_map, w_map;   // codes as bytes [rows][row bytes], box 128 x 128, 128-byte swizzle
-    CUtensorMap xs_map, ws_map; // scale tiles as 32-bit words [128-row blocks][256 per 256 columns], box 256 x 1
+    CUtensorMap x_map, w_map;   // codes as bytes [rows][row bytes], box 128 bytes x the rows a CTA loads,
+                                // 128-byte swizzle
+    CUtensorMap xs_map, ws_map; // scale tiles as 32-bit words [128-row blocks][256 per 256 columns], box 256 x
+                                // the blocks of a tile
     CUtensorMap b_map[4];       // the pool's B blocks, as in GemmParams
     int32_t b_col_div;
     void *Y;                    // [n_rows][ldy], written for every row
@@ -247,11 +251,13 @@ struct MxSlots {
     const int32_t *block_slots;
     const float *H;
     int64_t ldh;
+    int32_t early;              // everything but H is complete before the kernel can start
 };
 
+// Tiles of a form: rows and columns of Y per tile (128 x 128, the few-rows form; 256 x 256 or
+// 256 x 384, the many-rows one) and CTAs per tile of the few-rows form.
 struct MxPlan {
-    int tile;      // 1: the few-rows form (128 x 128 tiles), 0: the many-rows one (256 x 256 pair tiles)
-    int ksplit;    // CTAs per tile of the few-rows form
+    int rows, cols, ksplit;
 };
 MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out);
 
@@ -260,7 +266,8 @@ MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out);
 // one before them in the stream waited for, and that one itself, are complete.
 cudaError_t launch_mx_tile(const MxGemmParams &p, const MxSegments &sg, int rank_bucket_max, int ksplit,
                            cudaStream_t stream);
-cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int rank_bucket_max, cudaStream_t stream);
+cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int rank_bucket_max, int cols,
+                           cudaStream_t stream);
 cudaError_t prepare_mx_gemm();
 
 // ---- rows grouped by slot (rows.cu)

@@ -159,30 +159,31 @@ bool encode_rows_map(CUtensorMap *map, const void *base, int64_t rows, int64_t c
 }
 
 // Rows of packed 4-bit codes as bytes [rows, cols] with row stride ld (bytes), 128-byte
-// swizzle, box 128 bytes x 128 rows; what lies outside reads as zero codes.
-bool encode_codes_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld)
+// swizzle, box 128 bytes x box_rows; what lies outside reads as zero codes.
+bool encode_codes_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld,
+                      uint32_t box_rows)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (enc == nullptr || base == nullptr || rows <= 0 || cols <= 0) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
     cuuint64_t strides[1] = {(cuuint64_t)ld};
-    cuuint32_t box[2] = {128, 128};
+    cuuint32_t box[2] = {128, box_rows};
     cuuint32_t elem[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, elem,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Scale tiles as 32-bit words: per 128 rows one row of 256 words per 256 columns, box 256 x 1
-// (the two tiles of one K block); blocks past the last read as zeros.
-bool encode_scales_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols)
+// Scale tiles as 32-bit words: per 128 rows one row of 256 words per 256 columns, box 256 x blocks
+// (the two tiles of one K block, of one or more row blocks); what lies past the last reads as zeros.
+bool encode_scales_map(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, uint32_t blocks)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (enc == nullptr || base == nullptr || rows <= 0 || cols <= 0) return false;
     const cuuint64_t words = (cuuint64_t)((cols + 255) / 256) * 256;
     cuuint64_t dims[2] = {words, (cuuint64_t)((rows + 127) / 128)};
     cuuint64_t strides[1] = {words * 4};
-    cuuint32_t box[2] = {256, 1};
+    cuuint32_t box[2] = {256, blocks};
     cuuint32_t elem[2] = {1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void *>(base), dims, strides, box, elem,
                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -205,15 +206,15 @@ bool encode_b_map(CUtensorMap *map, const mlora_pool *pool, int R, int cols)
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// The wide view of the pool's B blocks (d_out a multiple of 32), box {256, 4, R/8, 1}.
-bool encode_b_map_wide(CUtensorMap *map, const mlora_pool *pool, int R)
+// The wide view of the pool's B blocks (d_out a multiple of 32), box {256, cols / 32, R/8, 1}.
+bool encode_b_map_wide(CUtensorMap *map, const mlora_pool *pool, int R, int cols = mlora::kExpandChunk)
 {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
     if (enc == nullptr || pool->d_out % 32 != 0) return false;
     const int groups = pool->r_bucket_max / 8;
     cuuint64_t dims[4] = {256, (cuuint64_t)pool->d_out / 32, (cuuint64_t)groups, (cuuint64_t)pool->n_slots};
     cuuint64_t strides[3] = {512, (cuuint64_t)pool->d_out * 16, (cuuint64_t)pool->slot_stride * 2};
-    cuuint32_t box[4] = {256, (cuuint32_t)mlora::kExpandChunk / 32, (cuuint32_t)(R / 8), 1};
+    cuuint32_t box[4] = {256, (cuuint32_t)cols / 32, (cuuint32_t)(R / 8), 1};
     cuuint32_t elem[4] = {1, 1, 1, 1};
     return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, pool->buf + pool->b_offset, dims, strides, box,
                elem, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
@@ -721,9 +722,7 @@ mlora_status mlora_base_gemm_apply(mlora_pool *pool, const mlora_segments *segs,
     p.ldx = ldx;
     p.H = H;
     p.ldh = rk;
-    if (mlora::launch_row_map(p, row_info, cs) != cudaSuccess ||
-        mlora::launch_block_slots(row_info, segs->n_rows, block_slots, cs) != cudaSuccess)
-        return MLORA_ERR_CUDA;
+    if (mlora::launch_row_blocks(p, row_info, block_slots, cs) != cudaSuccess) return MLORA_ERR_CUDA;
     // 2. H = X A^T for every valid segment (decode-shaped and long-segment kernels)
     const bool shrink = segs->n_segments > 0 && segs->n_tokens > 0;
     if (shrink) {
@@ -784,13 +783,14 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
 
     const mlora::MxPlan plan = mlora::plan_mx_gemm(Xq->n_rows, pool->d_in, pool->d_out);
-    const int tile = plan.tile ? mlora::kMxTileRows : 2 * mlora::kMxTileRows;   // rows and columns of a tile
+    const bool few = plan.rows == mlora::kMxTileRows;   // the few-rows form
+    const int b_cols = few ? 128 : plan.cols / 2;       // W rows (B columns) a CTA loads at a time
     mlora::MxGemmParams g{};
     const int64_t row_bytes = round_up(pool->d_in, 32) / 2;
-    if (!encode_codes_map(&g.x_map, Xq->codes, Xq->n_rows, row_bytes, Xq->ld) ||
-        !encode_codes_map(&g.w_map, W->codes, W->n_rows, row_bytes, W->ld) ||
-        !encode_scales_map(&g.xs_map, Xq->scales, Xq->n_rows, pool->d_in) ||
-        !encode_scales_map(&g.ws_map, W->scales, W->n_rows, pool->d_in))
+    if (!encode_codes_map(&g.x_map, Xq->codes, Xq->n_rows, row_bytes, Xq->ld, 128) ||
+        !encode_codes_map(&g.w_map, W->codes, W->n_rows, row_bytes, W->ld, b_cols) ||
+        !encode_scales_map(&g.xs_map, Xq->scales, Xq->n_rows, pool->d_in, 1) ||
+        !encode_scales_map(&g.ws_map, W->scales, W->n_rows, pool->d_in, plan.cols / 128))
         return MLORA_ERR_CUDA;
     g.Y = Y;
     g.ldy = ldy;
@@ -799,21 +799,27 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
     g.n_rows = Xq->n_rows;
     g.d_in = pool->d_in;
     g.d_out = pool->d_out;
-    g.n_mblk = (Xq->n_rows + tile - 1) / tile;
-    g.n_nblk = (pool->d_out + tile - 1) / tile;
+    g.n_mblk = (Xq->n_rows + plan.rows - 1) / plan.rows;
+    g.n_nblk = (pool->d_out + plan.cols - 1) / plan.cols;
     if (!lora) {
-        const cudaError_t e = plan.tile ? mlora::launch_mx_tile(g, mlora::MxSegments{}, 0, plan.ksplit, cs)
-                                        : mlora::launch_mx_pair(g, mlora::MxSlots{}, 0, cs);
+        const cudaError_t e = few ? mlora::launch_mx_tile(g, mlora::MxSegments{}, 0, plan.ksplit, cs)
+                                  : mlora::launch_mx_pair(g, mlora::MxSlots{}, 0, plan.cols, cs);
         return e == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
     }
-    for (int i = 0; i < 4; ++i) g.b_map[i] = pool->b_maps_wide_ok ? pool->b_maps_wide[i] : pool->b_maps[i];
+    for (int i = 0; i < 4; ++i) {
+        g.b_map[i] = pool->b_maps_wide_ok ? pool->b_maps_wide[i] : pool->b_maps[i];
+        if (b_cols != 128 && (8 << i) <= pool->r_bucket_max &&
+            !(pool->b_maps_wide_ok ? encode_b_map_wide(&g.b_map[i], pool, 8 << i, b_cols)
+                                   : encode_b_map(&g.b_map[i], pool, 8 << i, b_cols)))
+            return MLORA_ERR_CUDA;
+    }
     g.b_col_div = pool->b_maps_wide_ok ? 32 : 1;
 
     // workspace: H (grouped order); for the many-rows form the row map and the row blocks' slot lists
     const int rk = std::max(16, pool->r_bucket_max);
     const size_t h_bytes = (size_t)round_up((int64_t)segs->n_tokens * rk * 4, 256);
-    const size_t map_bytes = plan.tile ? 0 : (size_t)round_up((int64_t)segs->n_rows * 16, 256);
-    const size_t slot_bytes = plan.tile ? 0 : (size_t)g.n_mblk * mlora::kBlockSlotsPitch * 4;
+    const size_t map_bytes = few ? 0 : (size_t)round_up((int64_t)segs->n_rows * 16, 256);
+    const size_t slot_bytes = few ? 0 : (size_t)g.n_mblk * mlora::kBlockSlotsPitch * 4;
     std::lock_guard<std::mutex> lock(pool->ws_mutex);   // held until the kernels are launched
     st = ensure_workspace(pool, h_bytes + map_bytes + slot_bytes, cs);
     if (st != MLORA_OK) return st;
@@ -826,14 +832,13 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
     p.ldh = rk;
     int4 *row_info = reinterpret_cast<int4 *>(ws + h_bytes);
     int32_t *block_slots = reinterpret_cast<int32_t *>(ws + h_bytes + map_bytes);
-    if (!plan.tile && (mlora::launch_row_map(p, row_info, cs) != cudaSuccess ||
-                       mlora::launch_block_slots(row_info, segs->n_rows, block_slots, cs) != cudaSuccess))
-        return MLORA_ERR_CUDA;
+    if (!few && mlora::launch_row_blocks(p, row_info, block_slots, cs) != cudaSuccess) return MLORA_ERR_CUDA;
     st = launch(pool, segs, mlora::MODE_SHRINK, p, stream);
     if (st != MLORA_OK) return st;
     const cudaError_t e =
-        plan.tile ? mlora::launch_mx_tile(g, mlora::MxSegments{p, H, rk}, pool->r_bucket_max, plan.ksplit, cs)
-                  : mlora::launch_mx_pair(g, mlora::MxSlots{row_info, block_slots, H, rk}, pool->r_bucket_max, cs);
+        few ? mlora::launch_mx_tile(g, mlora::MxSegments{p, H, rk}, pool->r_bucket_max, plan.ksplit, cs)
+            : mlora::launch_mx_pair(g, mlora::MxSlots{row_info, block_slots, H, rk, long_path(pool, segs) ? 1 : 0},
+                                     pool->r_bucket_max, plan.cols, cs);
     return e == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
 }
 

@@ -11,7 +11,8 @@
 //
 // Two kernels.  Few rows are bound by the bytes of W and by latency: mx_tile_kernel, 128 x 128
 // tiles with d_in split over a cluster, so that all SMs stream W.  Many rows are bound by the
-// tensor core and the copies that feed it: mx_pair_kernel, 256 x 256 tiles on pairs of CTAs.
+// tensor core and the copies that feed it: mx_pair_kernel, 256 x 256 or 256 x 384 tiles
+// on pairs of CTAs.
 // Every mbarrier wait is bounded; on expiry a kernel flags a timeout and stores nothing.
 #include <algorithm>
 #include <mutex>
@@ -120,19 +121,25 @@ struct TileCtl {
     volatile int fail;
     int count;                     // distinct slots of the tile's rows, and their
     int slot[MR], bucket[MR];      // numbers and rank buckets
-    int pos[MR], row_slot[MR];     // each row's grouped position (-1: none) and slot
+    int pos[MR];                   // each row's grouped position (-1: none)
+    alignas(16) int row_slot[MR];  // and slot
     int part[4];
 };
 
+// Bounded wait; the flag of one that ran out is looked at only while waiting.
 __device__ __forceinline__ bool mwait(const MxGemmParams &p, TileCtl &ctl, uint64_t *bar, uint32_t parity)
 {
-    if (ctl.fail) return false;
-    if (!mbar_wait_bounded(bar, parity, kMxWaitNs)) {
-        ctl.fail = 1;
-        atomicOr(p.status, kFlagTimeout);
-        return false;
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (ctl.fail) return false;
+        if (global_timer_ns() - t0 > kMxWaitNs) break;
     }
-    return true;
+    ctl.fail = 1;
+    atomicOr(p.status, kFlagTimeout);
+    return false;
 }
 
 // The operand warps' 128 threads: row r's grouped position, slot, scale and rank (position -1:
@@ -151,42 +158,26 @@ __device__ int4 find_rows(const TileParams &t, TileCtl &ctl, int m0, int r, bool
             if (f) atomicOr(t.status, f);
         }
     }
-    // a position counts for its row if its segment is a valid adapter segment
-    int4 info = make_int4(-1, -1, 0, 0);
     for (int q0 = 0; q0 < t.n_tokens; q0 += 512) {
         int row[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const int q = q0 + 128 * u + r;
-            row[u] = q < t.n_tokens ? (t.token_indices ? t.token_indices[q] : q) : m0 - 1;
+            row[u] = q < t.n_tokens && t.token_indices ? t.token_indices[q] : q;
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int q = q0 + 128 * u + r, at = row[u] - m0;
-            const bool in = at >= 0 && at < MR && row[u] < t.n_rows;
-            if (q >= t.n_tokens || (!in && !(reporter && (row[u] < 0 || row[u] >= t.n_rows)))) continue;
-            const int g = segment_of_position(t, q);
-            const int a = t.slots[g], p0 = t.offsets[g], p1 = t.offsets[g + 1];
-            int rank = 0;
-            float scale = 0.f;
-            if (a < 0 || q < p0 || q >= p1 || segment_problem(t, g, a, p0, p1, rank, scale)) continue;
-            if (!in || atomicCAS(&ctl.pos[at], -1, q) != -1) atomicOr(t.status, kFlagBadRow);   // no row, or claimed twice
+            const int q = q0 + 128 * u + r;
+            const int at = q < t.n_tokens ? claimed_row(t, q, row[u], m0, MR, reporter) : -1;
+            if (at >= 0 && atomicCAS(&ctl.pos[at], -1, q) != -1) atomicOr(t.status, kFlagBadRow);   // claimed twice
         }
     }
     named_sync(kRowBar, 128);
-    const int q = ctl.pos[r];
-    if (q >= 0) {
-        const int g = segment_of_position(t, q);
-        int rank = 0;
-        float scale = 0.f;
-        segment_problem(t, g, t.slots[g], t.offsets[g], t.offsets[g + 1], rank, scale);
-        info = make_int4(q, t.slots[g], __float_as_int(scale), rank);
-    }
+    int4 info = make_int4(-1, -1, 0, 0);
+    if (ctl.pos[r] >= 0) info = row_of_position(t, ctl.pos[r]);
     ctl.row_slot[r] = info.y;
     named_sync(kRowBar, 128);
-    bool first = info.x >= 0;
-    for (int j = 0; j < r && first; ++j)
-        if (ctl.row_slot[j] == info.y) first = false;
+    const bool first = first_with_slot(ctl.row_slot, r, info.y);
     const unsigned m = __ballot_sync(0xffffffffu, first);
     if (lane == 0) ctl.part[warp] = __popc(m);
     named_sync(kRowBar, 128);
@@ -348,8 +339,8 @@ __global__ void __launch_bounds__(MT, 1)
             if (r == 0) mbar_arrive(&ctl.listed);
             const int cnt = ctl.count;
             lora = cnt > crank;   // this CTA has a slot
-            RowOperand<RK> op;
-            if (info.x >= 0) op.load(sg.H + (int64_t)info.x * sg.ldh, info.w, __int_as_float(info.z));
+            RowOperand<RK, 1> op;
+            if (info.x >= 0) op.load(sg.H + (int64_t)info.x * sg.ldh, info.w, __int_as_float(info.z), 0);
             bool dirty0 = false, dirty1 = false;   // this row of the buffer holds values
             uint32_t hc = 0;
             for (int j = crank; j < cnt; j += ksplit, ++hc) {
@@ -359,7 +350,7 @@ __global__ void __launch_bounds__(MT, 1)
                     break;
                 }
                 const bool mine = info.x >= 0 && info.y == ctl.slot[j];
-                if (mine || (hb ? dirty1 : dirty0)) op.store(hop + hb * 2 * HOP, r, mine);
+                if (mine || (hb ? dirty1 : dirty0)) op.store(hop + hb * 2 * HOP, r, 0, mine);
                 if (hb) dirty1 = mine;
                 else dirty0 = mine;
                 fence_proxy_async_smem();
@@ -439,43 +430,58 @@ __global__ void __launch_bounds__(MT, 1)
 }
 
 // ------------------------------------------------------------------ many rows
-// Persistent 256 x 256 tiles on pairs of CTAs (a cluster of two on neighbouring SMs) with
-// tcgen05.mma.cta_group::2: CTA c holds rows [128 c, +128) of the tile's X and of its W columns,
-// and 128 rows of the fp32 accumulator (256 columns of tensor memory; the rest holds the stages'
-// scales, so there is no room for a second accumulator).  The epilogue therefore takes the tile
-// out of tensor memory in one go, as 16-bit values in the registers of eight warps, hands the
-// accumulator back and stores while the next tile's products run.
-//   warp 0     TMA of both CTAs onto the even one's barriers, as in base_gemm.cu: per K block the
-//              CTA's codes of X and half of W's, its rows' scales of X and all 256 columns' of W
+// Persistent tiles of 256 rows x (NSUB x UN) columns on pairs of CTAs (a cluster of two on
+// neighbouring SMs) with tcgen05.mma.cta_group::2: CTA c holds rows [128 c, +128) of the tile's X,
+// half of the W rows of each sub-tile, and 128 rows of the fp32 accumulator.  The accumulator and
+// the stages' scales fill tensor memory, so there is no second accumulator: the epilogue takes
+// the tile out in one go, as 16-bit values in the registers of eight warps, hands it back and
+// stores while the next tile's products run.
+//   warp 0     TMA of both CTAs' codes onto the even one's barriers, as in base_gemm.cu: one box of X
+//              and one of W a stage.  warp 18: the scales, one box each.  What a thread issues
+//              takes it about 60 ns a copy however large, and with seven smaller boxes from one
+//              thread that was what a stage took (0.76 us at 384 columns)
 //   warp 1     even CTA: the products of the pair; after the K blocks it waits for them before the
 //              low-rank products, whose instruction kind differs, continue the same accumulator
-//   warps 2-5  offer the rows' s H slot by slot
-//   warps 6-13 epilogue: quarter = warp % 4 of the rows, half = (warp - 6) / 4 of the columns
+//   warps 2-9  bring the stages' scales from shared to tensor memory, two groups of four warps in
+//              turn, each warp its quarter of the lanes (the tensor core wants a copy in each).
+//              tcgen05.cp would do it from the products' thread, but takes its place in their
+//              pipe, about 100 cycles a tile of scales: 4096 x 8192 -> 28416 took 498 us with it,
+//              431 us so.  One group is not enough: a stage takes it 0.85 us, mostly latency
+//   warps 10-17 offer the rows' s H slot by slot, then the epilogue: quarter = warp % 4 of the
+//              rows, half = (warp - 10) / 4 of the ranks and of the columns
+// Sub-tile u's columns are [PH u, +PH) of each CTA's PN / 2, so that a CTA's W rows are one box.
 namespace {
 
-constexpr int PN = 256;                    // columns per tile
-constexpr int PH = 128;                    // W rows (and B columns) per CTA
-constexpr int P_STAGE = 2 * OP_BYTES + 3 * SF_BYTES + 1024;   // a multiple of 1 KB, as the swizzle wants
-constexpr int PT = 14 * 32;
-constexpr int P_SCALES = 256, P_COLS = 512;
-constexpr int P_SF_COLS = 24;              // 8 for X, 16 for W per stage
+constexpr int PT = 19 * 32;
+constexpr int P_COLS = 512;
 constexpr uint16_t kPairMask = 0x3;
 constexpr int kGroupRows = 8;              // row blocks per group of tiles (see tile_at)
+constexpr int kPairStages = 6;             // most ring stages of any shape
 
-template <int RK>
+template <int RK, int NSUB>
 struct PairShape {
+    static constexpr int UN = NSUB == 1 ? 256 : 192;   // columns per product
+    static constexpr int PN = NSUB * UN;               // columns per tile
+    static constexpr int PH = UN / 2;                  // W rows (and B columns) per CTA and sub-tile
+    static constexpr int W_BYTES = PN / 2 * KB / 2;    // a CTA's codes of W per stage
+    static constexpr int NSF = 1 + PN / 128;           // scale blocks (128 rows each) of a stage
+    static constexpr int SF_COLS = 8 * NSF;            // their columns of tensor memory
+    static constexpr int STAGE = OP_BYTES + W_BYTES + (NSF * SF_BYTES + 1023) / 1024 * 1024;
     static constexpr int HOP = MR * RK * 2;
     static constexpr int HB = RK == 64 ? 1 : 2;        // operand buffers
-    static constexpr int GS = RK ? 5 : 6;               // ring stages
+    static constexpr int GS = NSUB == 2 ? 4 : RK ? 5 : 6;   // ring stages
     static constexpr int ZERO = RK ? 2048 : 0;
-    static constexpr int SMEM = 1024 + GS * P_STAGE + HB * 2 * HOP + ZERO;
+    static constexpr int SMEM = 1024 + GS * STAGE + HB * 2 * HOP + ZERO;
     static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
-    static_assert(P_SCALES + P_SF_COLS * GS <= P_COLS, "tensor memory");
-    static_assert(P_STAGE % 1024 == 0 && PH * RK * 2 <= P_STAGE, "stage layout");
+    static_assert(PN + SF_COLS * GS <= P_COLS && GS <= kPairStages, "tensor memory");
+    static_assert(STAGE % 1024 == 0 && PN / 2 * RK * 2 <= STAGE, "stage layout");
 };
 
 struct PairCtl {
-    uint64_t full[6], empty[6];
+    // Ring stages, counted alike by all who use them (K blocks and slots' B chunks):
+    uint64_t full[kPairStages];    // the codes have landed, the scales are in both CTAs' tensor memory
+    uint64_t empty[kPairStages];   // the products are done
+    uint64_t local[kPairStages];   // this CTA's scales have landed
     uint64_t acc_full, acc_empty;
     uint64_t k_done;               // the K blocks' products are complete
     uint64_t hop_full[2], hop_empty[2];
@@ -483,17 +489,22 @@ struct PairCtl {
     volatile int fail;
 };
 
-// On expiry both CTAs of the pair are told to stop.
+// Bounded wait.  The flag of a wait that ran out, here or in the pair's other CTA (which is
+// told), is looked at only while waiting: a satisfied wait costs one test.
 __device__ __forceinline__ bool pwait(const MxGemmParams &p, PairCtl &ctl, uint64_t *bar, uint32_t parity)
 {
-    if (ctl.fail) return false;
-    if (!mbar_wait_bounded_cluster(bar, parity, kMxWaitNs)) {
-        ctl.fail = 1;
-        st_cluster_u32(map_to_rank(smem_addr((const void *)&ctl.fail), cluster_rank() ^ 1u), 1u);
-        atomicOr(p.status, kFlagTimeout);
-        return false;
+    if (mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait_cluster(bar, parity)) return true;
+        if (ctl.fail) return false;
+        if (global_timer_ns() - t0 > kMxWaitNs) break;
     }
-    return true;
+    ctl.fail = 1;
+    st_cluster_u32(map_to_rank(smem_addr((const void *)&ctl.fail), cluster_rank() ^ 1u), 1u);
+    atomicOr(p.status, kFlagTimeout);
+    return false;
 }
 
 // Tiles run in groups of kGroupRows row blocks, column-major inside a group, so that the pairs
@@ -506,6 +517,30 @@ __device__ __forceinline__ void tile_at(const MxGemmParams &p, int t, int &mb, i
     const int local = t % per_group;
     mb = first_mb + local % rows;
     nb = local / rows;
+}
+
+// A row block's distinct slots.  The count and the first two are read at once, when a tile
+// begins: after its K blocks their latency would be the tile's.
+struct SlotList {
+    const int32_t *list;
+    int count, slot0, bucket0, slot1, bucket1;
+    __device__ __forceinline__ int slot(int j) const { return j == 0 ? slot0 : j == 1 ? slot1 : list[1 + 2 * j]; }
+    __device__ __forceinline__ int bucket(int j) const { return j == 0 ? bucket0 : j == 1 ? bucket1 : list[2 + 2 * j]; }
+};
+
+template <int RK>
+__device__ __forceinline__ SlotList slot_list(const MxSlots &sl, int mb)
+{
+    SlotList s{};
+    if constexpr (RK > 0) {
+        s.list = sl.block_slots + (int64_t)mb * kBlockSlotsPitch;
+        s.count = s.list[0];
+        s.slot0 = s.list[1];
+        s.bucket0 = s.list[2];
+        s.slot1 = s.list[3];
+        s.bucket1 = s.list[4];
+    }
+    return s;
 }
 
 __device__ __forceinline__ uint32_t leader_bar(const uint64_t *bar) { return map_to_rank(smem_addr(bar), 0); }
@@ -532,20 +567,54 @@ __device__ __forceinline__ void transpose8(uint4 (&a)[8], int k)
     }
 }
 
+// 64 columns of this lane's row out of tensor memory, rounded to 16 bits: eight 16-byte pieces.
+template <int YT>
+__device__ __forceinline__ void take64(uint32_t taddr, uint4 (&a)[8])
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+        uint32_t v[32];
+        tmem_ld32(taddr + 32 * c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = pack2<YT>(__uint_as_float(v[8 * q + 2 * i]), __uint_as_float(v[8 * q + 2 * i + 1]));
+            a[4 * c + q] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// Stores 64 columns of the warp's rows; this lane's eight are at n0 + n, `gap` more from n = jump on.
+__device__ __forceinline__ void put64(const MxGemmParams &p, uint4 (&a)[8], int row0, int n0, int n, int jump, int gap,
+                                      int k)
+{
+    transpose8(a, k);
+    const int col = n0 + (n < jump ? n : n + gap);
+    if (col >= p.d_out) return;   // d_out is a multiple of 8
+    uint16_t *y = static_cast<uint16_t *>(p.Y) + col;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (row0 + j < p.n_rows) *reinterpret_cast<uint4 *>(y + (int64_t)(row0 + j) * p.ldy) = a[j];
+}
+
 }  // namespace
 
 // YT: 0 bf16, 1 fp16, 2 fp32 (an fp32 tile does not fit the epilogue's registers: it is stored
 // from tensor memory chunk by chunk, and the accumulator handed back after the last).
-template <int RK, int YT>
+template <int RK, int NSUB, int YT>
 __global__ void __launch_bounds__(PT, 1)
     mx_pair_kernel(const __grid_constant__ MxGemmParams p, const __grid_constant__ MxSlots sl)
 {
-    using S = PairShape<RK>;
-    constexpr int GS = S::GS, HOP = S::HOP, HB = S::HB;
+    using S = PairShape<RK, NSUB>;
+    constexpr int GS = S::GS, HOP = S::HOP, HB = S::HB, UN = S::UN, PN = S::PN, PH = S::PH;
+    constexpr int SF_AT = OP_BYTES + S::W_BYTES;   // scales in a stage: X's block, then W's
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ PairCtl ctl;
     uint8_t *ring = align_1024(smem_raw);
-    uint8_t *hop = ring + GS * P_STAGE;            // [HB][hi, lo]
+    uint8_t *hop = ring + GS * S::STAGE;           // [HB][hi, lo]
     uint8_t *zero = hop + HB * 2 * HOP;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int crank = (int)cluster_rank();         // 0 issues the pair's products
@@ -558,8 +627,9 @@ __global__ void __launch_bounds__(PT, 1)
     }
     if (tid == 0) {
         for (int s = 0; s < GS; ++s) {
-            mbar_init(&ctl.full[s], 1);
+            mbar_init(&ctl.full[s], 1 + 8);        // the producer, four scale warps in each CTA
             mbar_init(&ctl.empty[s], 1);
+            mbar_init(&ctl.local[s], 1);
         }
         mbar_init(&ctl.acc_full, 1);
         mbar_init(&ctl.acc_empty, 16);             // eight epilogue warps in each CTA
@@ -581,41 +651,39 @@ __global__ void __launch_bounds__(PT, 1)
     cluster_arrive_release();   // both CTAs' barriers exist before either signals the other's
     cluster_wait_acquire();
     tc_fence_after();
-    griddep_wait();
+    // After a long-segment shrink only the operand warps wait for the grids before this one: that
+    // shrink follows a plainly launched kernel, so all but H is complete when this one starts.
+    if (!sl.early || (warp >= 10 && warp < 18)) griddep_wait();
     const uint32_t tmem = ctl.tmem;
     const int n_tiles = p.n_mblk * p.n_nblk;
     const int nkb = (p.d_in + KB - 1) / KB;
 
+    // Ring stages are counted by g: a tile's K blocks, then its slots' B chunks.
     if (warp == 0) {
         if (lane == 0) {
             uint32_t g = 0;
             for (int t = first; t < n_tiles && !ctl.fail; t += n_clusters) {
                 int mb, nb;
                 tile_at(p, t, mb, nb);
-                const int m0 = (2 * mb + crank) * MR, nc = nb * PN + PH * crank;
+                const SlotList slots = slot_list<RK>(sl, mb);
+                const int m0 = (2 * mb + crank) * MR, nc = nb * PN + PN / 2 * crank;
                 for (int kb = 0; kb < nkb; ++kb, ++g) {
                     const int s = (int)(g % GS);
                     if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
-                    uint8_t *st = ring + s * P_STAGE;
-                    if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * (2 * OP_BYTES + 3 * SF_BYTES));
+                    uint8_t *st = ring + s * S::STAGE;
+                    if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * SF_AT);
                     const uint32_t fb = leader_bar(&ctl.full[s]);
-                    // rows past the end, and their scales, read as zeros
+                    // rows past the end read as zeros
                     tma_load_2d_pair(st, &p.x_map, kb * (KB / 2), m0, fb);
                     tma_load_2d_pair(st + OP_BYTES, &p.w_map, kb * (KB / 2), nc, fb);
-                    tma_load_2d_pair(st + 2 * OP_BYTES, &p.xs_map, kb * 256, 2 * mb + crank, fb);
-                    tma_load_2d_pair(st + 2 * OP_BYTES + SF_BYTES, &p.ws_map, kb * 256, 2 * nb, fb);
-                    tma_load_2d_pair(st + 2 * OP_BYTES + 2 * SF_BYTES, &p.ws_map, kb * 256, 2 * nb + 1, fb);
                 }
-                if constexpr (RK > 0) {
-                    const int32_t *bs = sl.block_slots + (int64_t)mb * kBlockSlotsPitch;
-                    const int cnt = bs[0];
-                    for (int j = 0; j < cnt && !ctl.fail; ++j, ++g) {
-                        const int slot = bs[1 + 2 * j], R = bs[2 + 2 * j], s = (int)(g % GS);
-                        if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
-                        if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * (uint32_t)R * PH * 2);
-                        tma_load_4d_pair(ring + s * P_STAGE, &p.b_map[bucket_index(R)], 0, nc / p.b_col_div, 0, slot,
-                                         leader_bar(&ctl.full[s]));
-                    }
+                for (int j = 0; j < slots.count && !ctl.fail; ++j, ++g) {
+                    const int slot = slots.slot(j), R = slots.bucket(j), s = (int)(g % GS);
+                    if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+                    // columns past d_out read as zeros
+                    if (leader) mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)R * PN * 2);
+                    tma_load_4d_pair(ring + s * S::STAGE, &p.b_map[bucket_index(R)], 0, nc / p.b_col_div, 0, slot,
+                                     leader_bar(&ctl.full[s]));
                 }
             }
         }
@@ -623,44 +691,45 @@ __global__ void __launch_bounds__(PT, 1)
     } else if (warp == 1) {
         if (leader && lane == 0) {
             uint32_t g = 0, hc = 0, tc = 0, kc = 0;
-            bool ok = true;
+            bool ok = true, ready = false;   // ready: the next stage was full when last looked at
             for (int t = first; t < n_tiles && ok; t += n_clusters, ++tc) {
                 int mb, nb;
                 tile_at(p, t, mb, nb);
-                for (int kb = 0; kb < nkb && ok; ++kb, ++g) {
+                const SlotList slots = slot_list<RK>(sl, mb);
+                if (tc > 0 && !pwait(p, ctl, &ctl.acc_empty, (tc - 1) & 1u)) break;
+                for (int kb = 0; kb < nkb; ++kb, ++g) {
                     const int s = (int)(g % GS);
-                    if (!pwait(p, ctl, &ctl.full[s], (g / GS) & 1u) ||
-                        (kb == 0 && tc > 0 && !pwait(p, ctl, &ctl.acc_empty, (tc - 1) & 1u))) {
+                    if (!ready && !pwait(p, ctl, &ctl.full[s], (g / GS) & 1u)) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint32_t xs = smem_addr(ring + s * P_STAGE), ws = xs + OP_BYTES, sf = xs + 2 * OP_BYTES;
-                    const uint32_t sx = tmem + P_SCALES + P_SF_COLS * s, sw = sx + 8;
-                    // per 128 of K: X's four columns; W's eight, for columns 0-127 and 128-255
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tmem_copy_scales<2>(sx + 4 * h, sf + 512 * h);
-                        tmem_copy_scales<2>(sw + 8 * h, sf + SF_BYTES + 512 * h);
-                        tmem_copy_scales<2>(sw + 8 * h + 4, sf + 2 * SF_BYTES + 512 * h);
-                    }
+                    const uint64_t xd = umma_desc_sw128(smem_addr(ring + s * S::STAGE));
+                    const uint64_t wd = xd + (OP_BYTES >> 4);   // (the address field, in 16 bytes)
+                    // per 128 of K: X's four columns of scales, then each sub-tile's (32 rows a column)
+                    const uint32_t sf = tmem + PN + S::SF_COLS * s;
                     const int steps = min(4, (p.d_in - kb * KB + 63) / 64);
-                    for (int k = 0; k < steps; ++k)
-                        umma_mxf4<2>(tmem, umma_desc_sw128(xs + 32 * k), umma_desc_sw128(ws + 32 * k),
-                                     umma_idesc_mxf4(2 * MR, PN, (k & 1) * 2, (k & 1) * 2), sx + 4 * (k >> 1),
-                                     sw + 8 * (k >> 1), kb > 0 || k > 0 ? 1u : 0u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        // a look at the next stage's barrier, while products are queued
+                        if (k == 2) ready = mbar_test_wait_cluster(&ctl.full[(g + 1) % GS], ((g + 1) / GS) & 1u);
+                        if (k >= steps) continue;
+                        const uint32_t sx = sf + (k >> 1) * 4 * S::NSF, sw = sx + 4;
+#pragma unroll
+                        for (int u = 0; u < NSUB; ++u)
+                            umma_mxf4<2>(tmem + u * UN, xd + 2 * k, wd + u * (PH * 128 >> 4) + 2 * k,
+                                         umma_idesc_mxf4(2 * MR, UN, (k & 1) * 2, (k & 1) * 2), sx, sw + u * UN / 32,
+                                         kb > 0 || k > 0 ? 1u : 0u);
+                    }
                     umma_commit_pair(&ctl.empty[s], kPairMask);
                 }
-                if constexpr (RK > 0) {
-                    const int32_t *bs = sl.block_slots + (int64_t)mb * kBlockSlotsPitch;
-                    const int cnt = ok ? bs[0] : 0;
-                    if (cnt > 0) {
-                        umma_commit_pair(&ctl.k_done, kPairMask);
-                        ok = pwait(p, ctl, &ctl.k_done, kc++ & 1u);
-                    }
-                    const uint32_t idesc = umma_idesc_bf16(2 * MR, PN);
-                    for (int j = 0; j < cnt && ok; ++j, ++g, ++hc) {
-                        const int R = bs[2 + 2 * j], s = (int)(g % GS), hb = (int)(hc % HB);
+                if (RK > 0 && ok && slots.count > 0) {
+                    umma_commit_pair(&ctl.k_done, kPairMask);
+                    ok = pwait(p, ctl, &ctl.k_done, kc++ & 1u);
+                    const uint32_t idesc = umma_idesc_bf16(2 * MR, UN);
+                    for (int j = 0; j < slots.count && ok; ++j, ++g, ++hc) {
+                        const int R = slots.bucket(j), s = (int)(g % GS), hb = (int)(hc % HB);
+                        ready = false;
                         if (!pwait(p, ctl, &ctl.hop_full[hb], (hc / HB) & 1u) ||
                             !pwait(p, ctl, &ctl.full[s], (g / GS) & 1u)) {
                             ok = false;
@@ -668,14 +737,20 @@ __global__ void __launch_bounds__(PT, 1)
                         }
                         tc_fence_after();
                         const uint32_t a_hi = smem_addr(hop + hb * 2 * HOP), a_lo = a_hi + HOP;
-                        const uint32_t b_s = smem_addr(ring + s * P_STAGE);
-                        for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
-                            const uint32_t b0 = b_s + st * 2 * PH * 16;
-                            const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PH * 16;
-                            const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
-                            const uint32_t koff = st * 2 * (MR / 8) * 128;
-                            umma_bf16_pair(tmem, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd, idesc, 1u);
-                            umma_bf16_pair(tmem, umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd, idesc, 1u);
+#pragma unroll
+                        for (int u = 0; u < NSUB; ++u) {
+                            const uint32_t b_s = smem_addr(ring + s * S::STAGE) + u * PH * 16;
+                            for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
+                                const uint32_t b0 = b_s + st * PN * 16;
+                                // bucket 8: the second rank group of B is the zero block
+                                const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PN / 2 * 16;
+                                const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
+                                const uint32_t koff = st * 2 * (MR / 8) * 128;
+                                umma_bf16_pair(tmem + u * UN, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd,
+                                               idesc, 1u);
+                                umma_bf16_pair(tmem + u * UN, umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd,
+                                               idesc, 1u);
+                            }
                         }
                         umma_commit_pair(&ctl.empty[s], kPairMask);
                         umma_commit_pair(&ctl.hop_empty[hb], kPairMask);
@@ -685,59 +760,127 @@ __global__ void __launch_bounds__(PT, 1)
             }
         }
         __syncwarp();
-    } else if (warp < 6) {
-        if constexpr (RK > 0) {
-            const int r = tid - 64;
-            const uint32_t full0 = leader_bar(&ctl.hop_full[0]), full1 = leader_bar(&ctl.hop_full[1]);
-            uint32_t hc = 0;
-            bool alive = true, dirty0 = false, dirty1 = false;
-            for (int t = first; t < n_tiles && alive; t += n_clusters) {
+    } else if (warp < 10) {
+        const uint32_t group = (uint32_t)(warp - 2) >> 2;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + PN;
+        uint32_t g = 0;
+        bool alive = true;
+        for (int t = first; t < n_tiles && alive; t += n_clusters) {
+            int mb, nb;
+            tile_at(p, t, mb, nb);
+            const int stages = nkb + slot_list<RK>(sl, mb).count;
+            for (int kb = 0; kb < stages; ++kb, ++g) {
+                const int s = (int)(g % GS);
+                if ((g & 1) != group) continue;
+                // (the products that last read these columns finished before the scales were fetched)
+                alive = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.local[s], (g / GS) & 1u));
+                if (!alive) break;
+                if (kb >= nkb) {   // a B chunk has no scales
+                    if (lane == 0) mbar_arrive_cluster(leader_bar(&ctl.full[s]));
+                    continue;
+                }
+                const uint8_t *src = ring + s * S::STAGE + SF_AT + lane * 16;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t w[4 * S::NSF];   // four 32-row groups of each block
+#pragma unroll
+                    for (int i = 0; i < S::NSF; ++i) {
+                        const uint4 v = *reinterpret_cast<const uint4 *>(src + i * SF_BYTES + h * 512);
+                        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
+                    }
+                    const uint32_t at = lanes + S::SF_COLS * s + 4 * S::NSF * h;
+                    if constexpr (NSUB == 1) {
+                        const uint32_t a[4] = {w[0], w[1], w[2], w[3]};
+                        const uint32_t b[8] = {w[4], w[5], w[6], w[7], w[8], w[9], w[10], w[11]};
+                        tmem_st4(at, a);
+                        tmem_st8(at + 4, b);
+                    } else {   // W's groups 0-2, 6-8 are sub-tile 0's columns, 3-5, 9-11 sub-tile 1's
+                        const uint32_t a[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[10]};
+                        const uint32_t b[8] = {w[11], w[12], w[7], w[8], w[9], w[13], w[14], w[15]};
+                        tmem_st8(at, a);
+                        tmem_st8(at + 8, b);
+                    }
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(leader_bar(&ctl.full[s]));
+            }
+        }
+    } else if (warp == 18) {
+        if (lane == 0) {
+            uint32_t g = 0;
+            for (int t = first; t < n_tiles && !ctl.fail; t += n_clusters) {
                 int mb, nb;
                 tile_at(p, t, mb, nb);
-                const int32_t *bs = sl.block_slots + (int64_t)mb * kBlockSlotsPitch;
-                const int cnt = bs[0];
-                if (cnt == 0) continue;
-                const int row = (2 * mb + crank) * MR + r;
-                int4 info = make_int4(-1, -1, 0, 0);
-                if (row < p.n_rows) info = sl.row_info[row];
-                RowOperand<RK> op;
-                if (info.x >= 0) op.load(sl.H + (int64_t)info.x * sl.ldh, info.w, __int_as_float(info.z));
-                for (int j = 0; j < cnt; ++j, ++hc) {
-                    const int hb = (int)(hc % HB);
-                    if (hc >= HB && !named_sync_and(kRowBar, 128, pwait(p, ctl, &ctl.hop_empty[hb], ((hc / HB) - 1) & 1u))) {
-                        alive = false;
-                        break;
+                const int stages = nkb + slot_list<RK>(sl, mb).count;
+                for (int kb = 0; kb < stages; ++kb, ++g) {
+                    const int s = (int)(g % GS);
+                    // (B chunks too: a waiter that skipped phases could not tell them apart by parity)
+                    if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+                    if (kb >= nkb) {
+                        mbar_arrive(&ctl.local[s]);
+                        continue;
                     }
-                    const bool mine = info.x >= 0 && info.y == bs[1 + 2 * j];
-                    if (mine || (hb ? dirty1 : dirty0)) op.store(hop + hb * 2 * HOP, r, mine);
-                    if (hb) dirty1 = mine;
-                    else dirty0 = mine;
-                    fence_proxy_async_smem();
-                    named_sync(kRowBar, 128);
-                    if (r == 0) mbar_arrive_cluster(hb ? full1 : full0);
+                    // blocks past the last read as zeros
+                    uint8_t *st = ring + s * S::STAGE + SF_AT;
+                    mbar_arrive_expect_tx(&ctl.local[s], S::NSF * SF_BYTES);
+                    tma_load_2d(st, &p.xs_map, kb * 256, 2 * mb + crank, &ctl.local[s]);
+                    tma_load_2d(st + SF_BYTES, &p.ws_map, kb * 256, nb * (PN / 128), &ctl.local[s]);
                 }
             }
         }
+        __syncwarp();
     } else {
-        const int quarter = warp & 3, half = (warp - 6) >> 2;
+        const int quarter = warp & 3, half = (warp - 10) >> 2;
         const uint32_t empty_bar = leader_bar(&ctl.acc_empty);
-        const int k = lane & 7;
-        uint32_t tc = 0;
-        for (int t = first; t < n_tiles; t += n_clusters, ++tc) {
+        const uint32_t hop_bar0 = leader_bar(&ctl.hop_full[0]), hop_bar1 = leader_bar(&ctl.hop_full[1]);
+        const int r = 32 * quarter + lane, k = lane & 7;
+        constexpr int HC = PN / 2;                 // columns per thread
+        bool dirty0 = false, dirty1 = false;       // this row of an operand buffer holds values
+        uint32_t tc = 0, hc = 0;
+        bool alive = true;
+        for (int t = first; t < n_tiles && alive; t += n_clusters, ++tc) {
             int mb, nb;
             tile_at(p, t, mb, nb);
-            if (!named_sync_and(kEpiBar, 256, pwait(p, ctl, &ctl.acc_full, tc & 1u))) break;
+            const int row = (2 * mb + crank) * MR + r;
+            if constexpr (RK > 0) {
+                // this tile's operand, while its K blocks run: this row, half of the ranks
+                const SlotList slots = slot_list<RK>(sl, mb);
+                int4 info = make_int4(-1, -1, 0, 0);
+                if (slots.count > 0 && row < p.n_rows) info = sl.row_info[row];
+                RowOperand<RK, 2> op;
+                if (info.x >= 0)
+                    op.load(sl.H + (int64_t)info.x * sl.ldh, info.w, __int_as_float(info.z), half);
+                for (int j = 0; j < slots.count; ++j, ++hc) {
+                    const int hb = (int)(hc % HB);
+                    if (hc >= HB &&
+                        !named_sync_and(kEpiBar, 256, pwait(p, ctl, &ctl.hop_empty[hb], ((hc / HB) - 1) & 1u))) {
+                        alive = false;
+                        break;
+                    }
+                    const bool mine = info.x >= 0 && info.y == slots.slot(j);
+                    if (mine || (hb ? dirty1 : dirty0)) op.store(hop + hb * 2 * HOP, r, half, mine);
+                    if (hb) dirty1 = mine;
+                    else dirty0 = mine;
+                    fence_proxy_async_smem();
+                    named_sync(kEpiBar, 256);
+                    if (warp == 10 && lane == 0) mbar_arrive_cluster(hb ? hop_bar1 : hop_bar0);
+                }
+            }
+            if (!named_sync_and(kEpiBar, 256, alive && pwait(p, ctl, &ctl.acc_full, tc & 1u))) break;
             tc_fence_after();
-            const int n0 = nb * PN + 128 * half;
-            const int warp_row = (2 * mb + crank) * MR + 32 * quarter;
-            const uint32_t tb = tmem + ((uint32_t)(32 * quarter) << 16) + 128 * half;
+            // accumulator column n of sub-tile u is column PH u + n of the tile, PN / 2 - PH more from
+            // n = PH on; with one sub-tile each half of the warps has half of its columns
+            const int n0 = nb * PN + (NSUB == 1 ? HC * half : PH * half), jump = NSUB == 1 ? HC : PH;
+            const int row0 = row - lane + 8 * (lane >> 3);
+            const uint32_t tb = tmem + ((uint32_t)(32 * quarter) << 16) + HC * half;
             if constexpr (YT == 2) {
-                const int row = warp_row + lane;
-                for (int c = 0; c < 128; c += 32) {
+                for (int c = 0; c < HC; c += 32) {
                     uint32_t v[32];
                     tmem_ld32(tb + c, v);
                     tmem_wait_ld();
-                    if (c == 96) {
+                    if (c == HC - 32) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0) mbar_arrive_cluster(empty_bar);
@@ -747,40 +890,25 @@ __global__ void __launch_bounds__(PT, 1)
                         float f[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * q + i]);
-                        if (row < p.n_rows && n0 + c + 8 * q < p.d_out) store8<2>(p, row, n0 + c + 8 * q, f);
+                        const int n = c + 8 * q, col = n0 + (n < jump ? n : n + PN / 2 - PH);
+                        if (row < p.n_rows && col < p.d_out) store8<2>(p, row, col, f);
                     }
                 }
             } else {
-                uint4 a[2][8];   // this lane's row, 128 columns
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    tmem_ld32(tb + 32 * c, v);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            w[i] = pack2<YT>(__uint_as_float(v[8 * q + 2 * i]), __uint_as_float(v[8 * q + 2 * i + 1]));
-                        a[c >> 1][(c & 1) * 4 + q] = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
+                // two pieces of 64 columns fit the registers; a third is stored first
+                if constexpr (HC == 192) {
+                    uint4 a[8];
+                    take64<YT>(tb + 128, a);
+                    put64(p, a, row0, n0, 128 + 8 * k, jump, PN / 2 - PH, k);
                 }
+                uint4 a[2][8];
+                take64<YT>(tb, a[0]);
+                take64<YT>(tb + 64, a[1]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(empty_bar);
-                const int row0 = warp_row + 8 * (lane >> 3);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    transpose8(a[h], k);
-                    const int col = n0 + 64 * h + 8 * k;
-                    if (col < p.d_out) {   // d_out is a multiple of 8
-                        uint16_t *y = static_cast<uint16_t *>(p.Y) + col;
-#pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            if (row0 + j < p.n_rows) *reinterpret_cast<uint4 *>(y + (int64_t)(row0 + j) * p.ldy) = a[h][j];
-                    }
-                }
+                put64(p, a[0], row0, n0, 8 * k, jump, PN / 2 - PH, k);
+                put64(p, a[1], row0, n0, 64 + 8 * k, jump, PN / 2 - PH, k);
             }
         }
     }
@@ -839,14 +967,23 @@ cudaError_t allow_smem(K kernel, int bytes)
     return cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100);
 }
 
+template <int RK, int NSUB>
+cudaError_t prepare_pair()
+{
+    constexpr int smem = PairShape<RK, NSUB>::SMEM;
+    cudaError_t e;
+    if ((e = allow_smem(mx_pair_kernel<RK, NSUB, 0>, smem)) != cudaSuccess) return e;
+    if ((e = allow_smem(mx_pair_kernel<RK, NSUB, 1>, smem)) != cudaSuccess) return e;
+    return allow_smem(mx_pair_kernel<RK, NSUB, 2>, smem);
+}
+
 template <int RK>
 cudaError_t prepare_rank()
 {
     cudaError_t e;
     if ((e = allow_smem(mx_tile_kernel<RK>, TileShape<RK>::SMEM)) != cudaSuccess) return e;
-    if ((e = allow_smem(mx_pair_kernel<RK, 0>, PairShape<RK>::SMEM)) != cudaSuccess) return e;
-    if ((e = allow_smem(mx_pair_kernel<RK, 1>, PairShape<RK>::SMEM)) != cudaSuccess) return e;
-    return allow_smem(mx_pair_kernel<RK, 2>, PairShape<RK>::SMEM);
+    if ((e = prepare_pair<RK, 1>()) != cudaSuccess) return e;
+    return prepare_pair<RK, 2>();
 }
 
 // Pairs resident at once on the current device (cached per device; every variant takes whole SMs).
@@ -859,10 +996,10 @@ cudaError_t active_pairs(int &active)
     std::lock_guard<std::mutex> lock(mu);
     if (cached[dev] == 0) {
         cudaLaunchAttribute attr[2];
-        cudaLaunchConfig_t cfg = config(2, PT, PairShape<0>::SMEM, 2, nullptr, attr);
+        cudaLaunchConfig_t cfg = config(2, PT, PairShape<0, 1>::SMEM, 2, nullptr, attr);
         cfg.numAttrs = 1;
         int n = 0;
-        cudaError_t e = cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<0, 0>, &cfg);
+        cudaError_t e = cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<0, 1, 0>, &cfg);
         if (e != cudaSuccess) return e;
         if (n <= 0) return cudaErrorInvalidConfiguration;
         cached[dev] = n;
@@ -871,14 +1008,20 @@ cudaError_t active_pairs(int &active)
     return cudaSuccess;
 }
 
-template <int RK>
-cudaError_t launch_pair(const MxGemmParams &p, const MxSlots &sl, unsigned pairs, cudaStream_t stream)
+template <int RK, int NSUB>
+cudaError_t launch_pair_shape(const MxGemmParams &p, const MxSlots &sl, unsigned pairs, cudaStream_t stream)
 {
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = config(2 * pairs, PT, PairShape<RK>::SMEM, 2, stream, attr);
-    if (p.y_type == 0) return cudaLaunchKernelEx(&cfg, mx_pair_kernel<RK, 0>, p, sl);
-    if (p.y_type == 1) return cudaLaunchKernelEx(&cfg, mx_pair_kernel<RK, 1>, p, sl);
-    return cudaLaunchKernelEx(&cfg, mx_pair_kernel<RK, 2>, p, sl);
+    const cudaLaunchConfig_t cfg = config(2 * pairs, PT, PairShape<RK, NSUB>::SMEM, 2, stream, attr);
+    if (p.y_type == 0) return cudaLaunchKernelEx(&cfg, mx_pair_kernel<RK, NSUB, 0>, p, sl);
+    if (p.y_type == 1) return cudaLaunchKernelEx(&cfg, mx_pair_kernel<RK, NSUB, 1>, p, sl);
+    return cudaLaunchKernelEx(&cfg, mx_pair_kernel<RK, NSUB, 2>, p, sl);
+}
+
+template <int RK>
+cudaError_t launch_pair(const MxGemmParams &p, const MxSlots &sl, int cols, unsigned pairs, cudaStream_t stream)
+{
+    return cols == 256 ? launch_pair_shape<RK, 1>(p, sl, pairs, stream) : launch_pair_shape<RK, 2>(p, sl, pairs, stream);
 }
 
 }  // namespace
@@ -890,7 +1033,7 @@ MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
     // block is two of those units of tensor-core work per SM.
     const int64_t nkb = (d_in + KB - 1) / KB;
     const int64_t tiles = (int64_t)((n_rows + 127) / 128) * ((d_out + MC - 1) / MC);
-    MxPlan plan{1, 1};
+    MxPlan plan{128, MC, 1};
     int64_t best = INT64_MAX;
     for (int ks = 1; ks <= 8 && ks <= nkb; ks *= 2) {
         const int64_t cost = (tiles * ks + 147) / 148 * ((nkb + ks - 1) / ks + 4) + (ks > 1 ? 2 : 0);
@@ -899,9 +1042,14 @@ MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
             plan.ksplit = ks;
         }
     }
-    const int64_t pairs = (int64_t)((n_rows + 255) / 256) * ((d_out + PN - 1) / PN);
-    const int64_t pair_cost = (pairs + 73) / 74 * (2 * nkb + 2) + 6;
-    plan.tile = pair_cost < best ? 0 : 1;
+    for (int cols = 256; cols <= 384; cols += 128) {
+        const int64_t pairs = (int64_t)((n_rows + 255) / 256) * ((d_out + cols - 1) / cols);
+        const int64_t cost = (pairs + 73) / 74 * (cols / 128 * nkb + 2) + 6;
+        if (cost < best) {
+            best = cost;
+            plan = MxPlan{256, cols, 1};
+        }
+    }
     return plan;
 }
 
@@ -913,15 +1061,16 @@ cudaError_t launch_mx_tile(const MxGemmParams &p, const MxSegments &sg, int rank
     return launch_tile<64>(p, sg, ksplit, stream);
 }
 
-cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int rank_bucket_max, cudaStream_t stream)
+cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int rank_bucket_max, int cols,
+                           cudaStream_t stream)
 {
     int active = 0;
     cudaError_t e = active_pairs(active);
     if (e != cudaSuccess) return e;
     const unsigned pairs = (unsigned)std::min<int64_t>((int64_t)p.n_mblk * p.n_nblk, active);
-    if (rank_bucket_max == 0) return launch_pair<0>(p, sl, pairs, stream);
-    if (rank_bucket_max <= 16) return launch_pair<16>(p, sl, pairs, stream);
-    return launch_pair<64>(p, sl, pairs, stream);
+    if (rank_bucket_max == 0) return launch_pair<0>(p, sl, cols, pairs, stream);
+    if (rank_bucket_max <= 16) return launch_pair<16>(p, sl, cols, pairs, stream);
+    return launch_pair<64>(p, sl, cols, pairs, stream);
 }
 
 cudaError_t prepare_mx_gemm()

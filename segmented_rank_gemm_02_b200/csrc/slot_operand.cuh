@@ -53,26 +53,29 @@ __device__ __forceinline__ void stage_operand(uint8_t *hi, uint8_t *lo, const fl
 
 // One row's s * H in registers, as the bf16 hi + lo parts that stage_operand writes, for kernels
 // that offer the operand slot by slot: a row belongs to one slot, so its values are loaded once
-// and written once, and the buffers are zero everywhere else.
-template <int RK>
+// and written once, and the buffers are zero everywhere else.  PARTS threads share a row, each
+// RK / PARTS of the ranks.
+template <int RK, int PARTS>
 struct RowOperand {
-    uint32_t hi[RK / 2], lo[RK / 2];
+    static constexpr int N = RK / PARTS;   // a multiple of 8
+    uint32_t hi[N / 2], lo[N / 2];
 
-    __device__ __forceinline__ void load(const float *hsrc, int rank, float sc)
+    __device__ __forceinline__ void load(const float *hsrc, int rank, float sc, int part)
     {
-        float h[RK];
+        const int c0 = part * N;
+        float h[N];
         if (rank == RK) {
 #pragma unroll
-            for (int i = 0; i < RK / 4; ++i) {
-                const float4 v = reinterpret_cast<const float4 *>(hsrc)[i];
+            for (int i = 0; i < N / 4; ++i) {
+                const float4 v = reinterpret_cast<const float4 *>(hsrc + c0)[i];
                 h[4 * i] = v.x, h[4 * i + 1] = v.y, h[4 * i + 2] = v.z, h[4 * i + 3] = v.w;
             }
         } else {
 #pragma unroll
-            for (int c = 0; c < RK; ++c) h[c] = c < rank ? hsrc[c] : 0.f;
+            for (int c = 0; c < N; ++c) h[c] = c0 + c < rank ? hsrc[c0 + c] : 0.f;
         }
 #pragma unroll
-        for (int c = 0; c < RK / 2; ++c) {
+        for (int c = 0; c < N / 2; ++c) {
             float h0, l0, h1, l1;
             split_bf16(sc * h[2 * c], h0, l0);
             split_bf16(sc * h[2 * c + 1], h1, l1);
@@ -82,12 +85,12 @@ struct RowOperand {
     }
 
     // Row r of a buffer (hi, then lo): the values, or zeros.
-    __device__ __forceinline__ void store(uint8_t *buf, int r, bool values) const
+    __device__ __forceinline__ void store(uint8_t *buf, int r, int part, bool values) const
     {
         constexpr int HOP = kOperandRows * RK * 2;
 #pragma unroll
-        for (int cg = 0; cg < RK / 8; ++cg) {
-            const int off = (cg * (kOperandRows / 8) + r / 8) * 128 + (r % 8) * 16;
+        for (int cg = 0; cg < N / 8; ++cg) {
+            const int off = ((part * (N / 8) + cg) * (kOperandRows / 8) + r / 8) * 128 + (r % 8) * 16;
             const uint4 z = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4 *>(buf + off) =
                 values ? make_uint4(hi[4 * cg], hi[4 * cg + 1], hi[4 * cg + 2], hi[4 * cg + 3]) : z;
@@ -123,6 +126,48 @@ __device__ __forceinline__ int segment_of_position(const TileParams &p, int q)
         else hi = mid - 1;
     }
     return lo;
+}
+
+// Grouped position q's claim on a row of [row0, row0 + n): the position's row if its segment is a
+// valid adapter segment.  `reporter` flags rows that do not exist; returns the row's index in the
+// block, or -1.
+__device__ __forceinline__ int claimed_row(const TileParams &p, int q, int row, int row0, int n, bool reporter)
+{
+    const bool exists = row >= 0 && row < p.n_rows;
+    const bool in = exists && row >= row0 && row < row0 + n;
+    if (!in && !(reporter && !exists)) return -1;
+    const int g = segment_of_position(p, q);
+    const int a = p.slots[g], p0 = p.offsets[g], p1 = p.offsets[g + 1];
+    int rank = 0;
+    float scale = 0.f;
+    if (a < 0 || q < p0 || q >= p1 || segment_problem(p, g, a, p0, p1, rank, scale)) return -1;
+    if (in) return row - row0;
+    atomicOr(p.status, kFlagBadRow);
+    return -1;
+}
+
+// {position, slot, scale, rank} of a claimed position.
+__device__ __forceinline__ int4 row_of_position(const TileParams &p, int q)
+{
+    const int g = segment_of_position(p, q), a = p.slots[g];
+    int rank = 0;
+    float scale = 0.f;
+    segment_problem(p, g, a, p.offsets[g], p.offsets[g + 1], rank, scale);
+    return make_int4(q, a, __float_as_int(scale), rank);
+}
+
+// Whether row r is the first of its block with this slot (>= 0); slots[] in shared memory,
+// 16-byte aligned, and the whole warp takes part.
+__device__ __forceinline__ bool first_with_slot(const int *slots, int r, int slot)
+{
+    const unsigned same = __match_any_sync(0xffffffffu, slot);
+    if (slot < 0 || (r & 31) != __ffs(same) - 1) return false;
+    const int4 *v = reinterpret_cast<const int4 *>(slots);
+    for (int i = 0; i < (r & ~31) / 4; ++i) {
+        const int4 s = v[i];
+        if (s.x == slot || s.y == slot || s.z == slot || s.w == slot) return false;
+    }
+    return true;
 }
 
 }  // namespace mlora
