@@ -276,42 +276,49 @@ __global__ void __launch_bounds__(MT, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            uint32_t g = 0, hc = 0;
-            bool ok = true;
-            for (int kb = kb0; kb < kb1; ++kb, ++g) {
-                const int s = (int)(g % GS);
-                if (!mwait(p, ctl, &ctl.full[s], (g / GS) & 1u)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t xs = smem_addr(ring + s * STAGE), ws = xs + OP_BYTES, sf = xs + 2 * OP_BYTES;
-                // the stage's own scale columns: their last readers finished before the stage was refilled
-                const uint32_t sx = tmem + T_SCALES + 16 * s, sw = sx + 8;
+        // (as in the pair kernel: the whole warp walks the stages, one lane issues)
+        const bool issuer = elect_one();
+        const uint64_t x0 = umma_desc_sw128(smem_addr(ring));
+        uint32_t g = 0, hc = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb, ++g) {
+            const int s = (int)(g % GS);
+            if (!__all_sync(0xffffffffu, mwait(p, ctl, &ctl.full[s], (g / GS) & 1u))) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const uint64_t xd = x0 + (uint32_t)s * (STAGE >> 4), wd = xd + (OP_BYTES >> 4);
+            const uint32_t sf = smem_addr(ring) + (uint32_t)s * STAGE + 2 * OP_BYTES;
+            // the stage's own scale columns: their last readers finished before the stage was refilled
+            const uint32_t sx = tmem + T_SCALES + 16 * s, sw = sx + 8;
+            const int steps = min(4, (p.d_in - kb * KB + 63) / 64);
+            if (issuer) {
                 tmem_copy_scales<1>(sx, sf);
                 tmem_copy_scales<1>(sx + 4, sf + 512);
                 tmem_copy_scales<1>(sw, sf + SF_BYTES);
                 tmem_copy_scales<1>(sw + 4, sf + SF_BYTES + 512);
-                const int steps = min(4, (p.d_in - kb * KB + 63) / 64);
-                for (int k = 0; k < steps; ++k)
-                    umma_mxf4<1>(tmem, umma_desc_sw128(xs + 32 * k), umma_desc_sw128(ws + 32 * k),
-                                 umma_idesc_mxf4(MR, MC, (k & 1) * 2, (k & 1) * 2), sx + 4 * (k >> 1), sw + 4 * (k >> 1),
-                                 kb > kb0 || k > 0 ? 1u : 0u);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (k < steps)
+                        umma_mxf4<1>(tmem, xd + 2 * k, wd + 2 * k, umma_idesc_mxf4(MR, MC, (k & 1) * 2, (k & 1) * 2),
+                                     sx + 4 * (k >> 1), sw + 4 * (k >> 1), kb > kb0 || k > 0 ? 1u : 0u);
                 umma_commit(&ctl.empty[s]);
             }
-            if (RK > 0 && ok) ok = mwait(p, ctl, &ctl.listed, 0);
-            if (RK > 0 && ok) {
-                const uint32_t idesc = umma_idesc_bf16(MR, MC);
-                const int cnt = ctl.count;
-                for (int j = crank; j < cnt; j += ksplit, ++g, ++hc) {
-                    const int R = ctl.bucket[j];
-                    const int s = (int)(g % GS), hb = (int)(hc & 1);
-                    if (!mwait(p, ctl, &ctl.hop_full[hb], (hc >> 1) & 1u) || !mwait(p, ctl, &ctl.full[s], (g / GS) & 1u)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
+            __syncwarp();
+        }
+        if (RK > 0 && ok) ok = __all_sync(0xffffffffu, mwait(p, ctl, &ctl.listed, 0));
+        if (RK > 0 && ok) {
+            constexpr uint32_t idesc = umma_idesc_bf16(MR, MC);
+            const int cnt = ctl.count;
+            for (int j = crank; j < cnt; j += ksplit, ++g, ++hc) {
+                const int R = ctl.bucket[j];
+                const int s = (int)(g % GS), hb = (int)(hc & 1);
+                ok = __all_sync(0xffffffffu, mwait(p, ctl, &ctl.hop_full[hb], (hc >> 1) & 1u) &&
+                                                 mwait(p, ctl, &ctl.full[s], (g / GS) & 1u));
+                if (!ok) break;
+                tc_fence_after();
+                if (issuer) {
                     const uint32_t a_hi = smem_addr(hop + hb * 2 * HOP), a_lo = a_hi + HOP;
                     const uint32_t b_s = smem_addr(ring + s * STAGE);
                     for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
@@ -327,9 +334,10 @@ __global__ void __launch_bounds__(MT, 1)
                     umma_commit(&ctl.empty[s]);
                     umma_commit(&ctl.hop_empty[hb]);
                 }
+                __syncwarp();
             }
-            if (ok) umma_commit(&ctl.done);
         }
+        if (ok && issuer) umma_commit(&ctl.done);
         __syncwarp();
     } else {
         const int r = tid - 64, quarter = warp & 3;
@@ -689,74 +697,91 @@ __global__ void __launch_bounds__(PT, 1)
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (leader && lane == 0) {
+        // The whole warp walks the stages, one lane of it issues: the descriptors then live in uniform
+        // registers, where the products take them from (one lane alone spent about 110 cycles a
+        // product on moving them there, more than the products of a 192-column sub-tile take).
+        if (leader) {
+            const bool issuer = elect_one();
+            const uint64_t x0 = umma_desc_sw128(smem_addr(ring));
             uint32_t g = 0, hc = 0, tc = 0, kc = 0;
             bool ok = true, ready = false;   // ready: the next stage was full when last looked at
             for (int t = first; t < n_tiles && ok; t += n_clusters, ++tc) {
                 int mb, nb;
                 tile_at(p, t, mb, nb);
                 const SlotList slots = slot_list<RK>(sl, mb);
-                if (tc > 0 && !pwait(p, ctl, &ctl.acc_empty, (tc - 1) & 1u)) break;
+                if (tc > 0 && !__all_sync(0xffffffffu, pwait(p, ctl, &ctl.acc_empty, (tc - 1) & 1u))) break;
                 for (int kb = 0; kb < nkb; ++kb, ++g) {
                     const int s = (int)(g % GS);
-                    if (!ready && !pwait(p, ctl, &ctl.full[s], (g / GS) & 1u)) {
+                    if (!ready && !__all_sync(0xffffffffu, pwait(p, ctl, &ctl.full[s], (g / GS) & 1u))) {
                         ok = false;
                         break;
                     }
                     tc_fence_after();
-                    const uint64_t xd = umma_desc_sw128(smem_addr(ring + s * S::STAGE));
-                    const uint64_t wd = xd + (OP_BYTES >> 4);   // (the address field, in 16 bytes)
+                    const uint64_t xd = x0 + (uint32_t)s * (S::STAGE >> 4);   // (the address field, in 16 bytes)
+                    const uint64_t wd = xd + (OP_BYTES >> 4);
                     // per 128 of K: X's four columns of scales, then each sub-tile's (32 rows a column)
                     const uint32_t sf = tmem + PN + S::SF_COLS * s;
                     const int steps = min(4, (p.d_in - kb * KB + 63) / 64);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        // a look at the next stage's barrier, while products are queued
-                        if (k == 2) ready = mbar_test_wait_cluster(&ctl.full[(g + 1) % GS], ((g + 1) / GS) & 1u);
-                        if (k >= steps) continue;
-                        const uint32_t sx = sf + (k >> 1) * 4 * S::NSF, sw = sx + 4;
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t sx = sf + h * 4 * S::NSF, sw = sx + 4;
+                        if (issuer) {
 #pragma unroll
-                        for (int u = 0; u < NSUB; ++u)
-                            umma_mxf4<2>(tmem + u * UN, xd + 2 * k, wd + u * (PH * 128 >> 4) + 2 * k,
-                                         umma_idesc_mxf4(2 * MR, UN, (k & 1) * 2, (k & 1) * 2), sx, sw + u * UN / 32,
-                                         kb > 0 || k > 0 ? 1u : 0u);
+                            for (int k = 2 * h; k < 2 * h + 2; ++k) {
+                                if (k >= steps) continue;
+#pragma unroll
+                                for (int u = 0; u < NSUB; ++u)
+                                    umma_mxf4<2>(tmem + u * UN, xd + 2 * k, wd + u * (PH * 128 >> 4) + 2 * k,
+                                                 umma_idesc_mxf4(2 * MR, UN, (k & 1) * 2, (k & 1) * 2), sx,
+                                                 sw + u * UN / 32, kb > 0 || k > 0 ? 1u : 0u);
+                            }
+                        }
+                        __syncwarp();
+                        // a look at the next stage's barrier, while products are queued
+                        if (h == 0)
+                            ready = __all_sync(0xffffffffu, mbar_test_wait_cluster(&ctl.full[(g + 1) % GS],
+                                                                                   ((g + 1) / GS) & 1u));
                     }
-                    umma_commit_pair(&ctl.empty[s], kPairMask);
+                    if (issuer) umma_commit_pair(&ctl.empty[s], kPairMask);
+                    __syncwarp();
                 }
                 if (RK > 0 && ok && slots.count > 0) {
-                    umma_commit_pair(&ctl.k_done, kPairMask);
-                    ok = pwait(p, ctl, &ctl.k_done, kc++ & 1u);
-                    const uint32_t idesc = umma_idesc_bf16(2 * MR, UN);
+                    if (issuer) umma_commit_pair(&ctl.k_done, kPairMask);
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.k_done, kc++ & 1u));
+                    constexpr uint32_t idesc = umma_idesc_bf16(2 * MR, UN);
                     for (int j = 0; j < slots.count && ok; ++j, ++g, ++hc) {
                         const int R = slots.bucket(j), s = (int)(g % GS), hb = (int)(hc % HB);
                         ready = false;
-                        if (!pwait(p, ctl, &ctl.hop_full[hb], (hc / HB) & 1u) ||
-                            !pwait(p, ctl, &ctl.full[s], (g / GS) & 1u)) {
-                            ok = false;
-                            break;
-                        }
+                        ok = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.hop_full[hb], (hc / HB) & 1u) &&
+                                                         pwait(p, ctl, &ctl.full[s], (g / GS) & 1u));
+                        if (!ok) break;
                         tc_fence_after();
-                        const uint32_t a_hi = smem_addr(hop + hb * 2 * HOP), a_lo = a_hi + HOP;
+                        if (issuer) {
+                            const uint32_t a_hi = smem_addr(hop + hb * 2 * HOP), a_lo = a_hi + HOP;
 #pragma unroll
-                        for (int u = 0; u < NSUB; ++u) {
-                            const uint32_t b_s = smem_addr(ring + s * S::STAGE) + u * PH * 16;
-                            for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
-                                const uint32_t b0 = b_s + st * PN * 16;
-                                // bucket 8: the second rank group of B is the zero block
-                                const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PN / 2 * 16;
-                                const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
-                                const uint32_t koff = st * 2 * (MR / 8) * 128;
-                                umma_bf16_pair(tmem + u * UN, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd,
-                                               idesc, 1u);
-                                umma_bf16_pair(tmem + u * UN, umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd,
-                                               idesc, 1u);
+                            for (int u = 0; u < NSUB; ++u) {
+                                const uint32_t b_s = smem_addr(ring + s * S::STAGE) + u * PH * 16;
+                                for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
+                                    const uint32_t b0 = b_s + st * PN * 16;
+                                    // bucket 8: the second rank group of B is the zero block
+                                    const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PN / 2 * 16;
+                                    const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
+                                    const uint32_t koff = st * 2 * (MR / 8) * 128;
+                                    umma_bf16_pair(tmem + u * UN, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd,
+                                                   idesc, 1u);
+                                    umma_bf16_pair(tmem + u * UN, umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd,
+                                                   idesc, 1u);
+                                }
                             }
+                            umma_commit_pair(&ctl.empty[s], kPairMask);
+                            umma_commit_pair(&ctl.hop_empty[hb], kPairMask);
                         }
-                        umma_commit_pair(&ctl.empty[s], kPairMask);
-                        umma_commit_pair(&ctl.hop_empty[hb], kPairMask);
+                        __syncwarp();
                     }
                 }
-                if (ok) umma_commit_pair(&ctl.acc_full, kPairMask);
+                if (ok && issuer) umma_commit_pair(&ctl.acc_full, kPairMask);
+                __syncwarp();
             }
         }
         __syncwarp();

@@ -102,6 +102,18 @@ __device__ __forceinline__ bool named_sync_and(uint32_t id, uint32_t nthreads, b
     return out != 0;
 }
 
+// True in one lane of the (converged) warp, always the same one.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(p));
+    return p != 0;
+}
+
 // ---------------------------------------------------------------- bulk copies
 // global -> this CTA's shared memory, completion counted in bytes on `bar`.
 __device__ __forceinline__ void bulk_load(void *dst_smem, const void *src_gmem, uint32_t bytes,
