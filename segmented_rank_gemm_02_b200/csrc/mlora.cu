@@ -784,7 +784,7 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
 
     const mlora::MxPlan plan = mlora::plan_mx_gemm(Xq->n_rows, pool->d_in, pool->d_out);
     const bool few = plan.rows == mlora::kMxTileRows;   // the few-rows form
-    const int b_cols = few ? 128 : plan.cols / 2;       // W rows (B columns) a CTA loads at a time
+    const int b_cols = plan.cols == 384 ? 96 : 128;     // W rows (B columns) a CTA loads at a time
     mlora::MxGemmParams g{};
     const int64_t row_bytes = round_up(pool->d_in, 32) / 2;
     if (!encode_codes_map(&g.x_map, Xq->codes, Xq->n_rows, row_bytes, Xq->ld, 128) ||

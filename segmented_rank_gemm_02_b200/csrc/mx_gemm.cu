@@ -444,23 +444,16 @@ __global__ void __launch_bounds__(MT, 1)
 // the stages' scales fill tensor memory, so there is no second accumulator: the epilogue takes
 // the tile out in one go, as 16-bit values in the registers of eight warps, hands it back and
 // stores while the next tile's products run.
-//   warp 0     TMA of both CTAs' codes onto the even one's barriers, as in base_gemm.cu: one box of X
-//              and one of W a stage.  warp 18: the scales, one box each.  What a thread issues
-//              takes it about 60 ns a copy however large, and with seven smaller boxes from one
-//              thread that was what a stage took (0.76 us at 384 columns)
-//   warp 1     even CTA: the products of the pair; after the K blocks it waits for them before the
+//   warp 0     TMA of both CTAs' codes onto the even one's barriers, as in base_gemm.cu
+//   warp 2     the scales likewise: one box of X's and one of W's a stage
+//   warp 1     even CTA: copies a stage's scales into that stage's own columns of tensor memory
+//              and issues the pair's products; after the K blocks it waits for them before the
 //              low-rank products, whose instruction kind differs, continue the same accumulator
-//   warps 2-9  bring the stages' scales from shared to tensor memory, two groups of four warps in
-//              turn, each warp its quarter of the lanes (the tensor core wants a copy in each).
-//              tcgen05.cp would do it from the products' thread, but takes its place in their
-//              pipe, about 100 cycles a tile of scales: 4096 x 8192 -> 28416 took 498 us with it,
-//              431 us so.  One group is not enough: a stage takes it 0.85 us, mostly latency
-//   warps 10-17 offer the rows' s H slot by slot, then the epilogue: quarter = warp % 4 of the
-//              rows, half = (warp - 10) / 4 of the ranks and of the columns
-// Sub-tile u's columns are [PH u, +PH) of each CTA's PN / 2, so that a CTA's W rows are one box.
+//   warps 4-11 offer the rows' s H slot by slot, then the epilogue: quarter = warp % 4 of the
+//              rows, half = (warp - 4) / 4 of the ranks and of the columns
 namespace {
 
-constexpr int PT = 19 * 32;
+constexpr int PT = 12 * 32;
 constexpr int P_COLS = 512;
 constexpr uint16_t kPairMask = 0x3;
 constexpr int kGroupRows = 8;              // row blocks per group of tiles (see tile_at)
@@ -471,10 +464,10 @@ struct PairShape {
     static constexpr int UN = NSUB == 1 ? 256 : 192;   // columns per product
     static constexpr int PN = NSUB * UN;               // columns per tile
     static constexpr int PH = UN / 2;                  // W rows (and B columns) per CTA and sub-tile
-    static constexpr int W_BYTES = PN / 2 * KB / 2;    // a CTA's codes of W per stage
+    static constexpr int W_BYTES = PH * KB / 2;        // a sub-tile's, a multiple of 1 KB
     static constexpr int NSF = 1 + PN / 128;           // scale blocks (128 rows each) of a stage
     static constexpr int SF_COLS = 8 * NSF;            // their columns of tensor memory
-    static constexpr int STAGE = OP_BYTES + W_BYTES + (NSF * SF_BYTES + 1023) / 1024 * 1024;
+    static constexpr int STAGE = OP_BYTES + NSUB * W_BYTES + (NSF * SF_BYTES + 1023) / 1024 * 1024;
     static constexpr int HOP = MR * RK * 2;
     static constexpr int HB = RK == 64 ? 1 : 2;        // operand buffers
     static constexpr int GS = NSUB == 2 ? 4 : RK ? 5 : 6;   // ring stages
@@ -482,14 +475,13 @@ struct PairShape {
     static constexpr int SMEM = 1024 + GS * STAGE + HB * 2 * HOP + ZERO;
     static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
     static_assert(PN + SF_COLS * GS <= P_COLS && GS <= kPairStages, "tensor memory");
-    static_assert(STAGE % 1024 == 0 && PN / 2 * RK * 2 <= STAGE, "stage layout");
+    static_assert(STAGE % 1024 == 0 && NSUB * PH * RK * 2 <= STAGE, "stage layout");
 };
 
 struct PairCtl {
     // Ring stages, counted alike by all who use them (K blocks and slots' B chunks):
-    uint64_t full[kPairStages];    // the codes have landed, the scales are in both CTAs' tensor memory
+    uint64_t full[kPairStages];    // the copies have landed
     uint64_t empty[kPairStages];   // the products are done
-    uint64_t local[kPairStages];   // this CTA's scales have landed
     uint64_t acc_full, acc_empty;
     uint64_t k_done;               // the K blocks' products are complete
     uint64_t hop_full[2], hop_empty[2];
@@ -579,11 +571,13 @@ __device__ __forceinline__ void transpose8(uint4 (&a)[8], int k)
 template <int YT>
 __device__ __forceinline__ void take64(uint32_t taddr, uint4 (&a)[8])
 {
+    uint32_t v2[2][32];
+    tmem_ld32(taddr, v2[0]);
+    tmem_ld32(taddr + 32, v2[1]);
+    tmem_wait_ld();
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-        uint32_t v[32];
-        tmem_ld32(taddr + 32 * c, v);
-        tmem_wait_ld();
+        const uint32_t (&v)[32] = v2[c];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t w[4];
@@ -595,12 +589,10 @@ __device__ __forceinline__ void take64(uint32_t taddr, uint4 (&a)[8])
     }
 }
 
-// Stores 64 columns of the warp's rows; this lane's eight are at n0 + n, `gap` more from n = jump on.
-__device__ __forceinline__ void put64(const MxGemmParams &p, uint4 (&a)[8], int row0, int n0, int n, int jump, int gap,
-                                      int k)
+__device__ __forceinline__ void put64(const MxGemmParams &p, uint4 (&a)[8], int row0, int n0, int k)
 {
     transpose8(a, k);
-    const int col = n0 + (n < jump ? n : n + gap);
+    const int col = n0 + 8 * k;
     if (col >= p.d_out) return;   // d_out is a multiple of 8
     uint16_t *y = static_cast<uint16_t *>(p.Y) + col;
 #pragma unroll
@@ -618,7 +610,7 @@ __global__ void __launch_bounds__(PT, 1)
 {
     using S = PairShape<RK, NSUB>;
     constexpr int GS = S::GS, HOP = S::HOP, HB = S::HB, UN = S::UN, PN = S::PN, PH = S::PH;
-    constexpr int SF_AT = OP_BYTES + S::W_BYTES;   // scales in a stage: X's block, then W's
+    constexpr int SF_AT = OP_BYTES + NSUB * S::W_BYTES;   // scales in a stage: X's block, then W's
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ PairCtl ctl;
     uint8_t *ring = align_1024(smem_raw);
@@ -635,9 +627,8 @@ __global__ void __launch_bounds__(PT, 1)
     }
     if (tid == 0) {
         for (int s = 0; s < GS; ++s) {
-            mbar_init(&ctl.full[s], 1 + 8);        // the producer, four scale warps in each CTA
+            mbar_init(&ctl.full[s], 2);            // codes, scales
             mbar_init(&ctl.empty[s], 1);
-            mbar_init(&ctl.local[s], 1);
         }
         mbar_init(&ctl.acc_full, 1);
         mbar_init(&ctl.acc_empty, 16);             // eight epilogue warps in each CTA
@@ -661,7 +652,7 @@ __global__ void __launch_bounds__(PT, 1)
     tc_fence_after();
     // After a long-segment shrink only the operand warps wait for the grids before this one: that
     // shrink follows a plainly launched kernel, so all but H is complete when this one starts.
-    if (!sl.early || (warp >= 10 && warp < 18)) griddep_wait();
+    if (!sl.early || warp >= 4) griddep_wait();
     const uint32_t tmem = ctl.tmem;
     const int n_tiles = p.n_mblk * p.n_nblk;
     const int nkb = (p.d_in + KB - 1) / KB;
@@ -674,7 +665,7 @@ __global__ void __launch_bounds__(PT, 1)
                 int mb, nb;
                 tile_at(p, t, mb, nb);
                 const SlotList slots = slot_list<RK>(sl, mb);
-                const int m0 = (2 * mb + crank) * MR, nc = nb * PN + PN / 2 * crank;
+                const int m0 = (2 * mb + crank) * MR, nc = nb * PN + PH * crank;
                 for (int kb = 0; kb < nkb; ++kb, ++g) {
                     const int s = (int)(g % GS);
                     if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
@@ -683,15 +674,44 @@ __global__ void __launch_bounds__(PT, 1)
                     const uint32_t fb = leader_bar(&ctl.full[s]);
                     // rows past the end read as zeros
                     tma_load_2d_pair(st, &p.x_map, kb * (KB / 2), m0, fb);
-                    tma_load_2d_pair(st + OP_BYTES, &p.w_map, kb * (KB / 2), nc, fb);
+#pragma unroll
+                    for (int u = 0; u < NSUB; ++u)
+                        tma_load_2d_pair(st + OP_BYTES + u * S::W_BYTES, &p.w_map, kb * (KB / 2), nc + u * UN, fb);
                 }
                 for (int j = 0; j < slots.count && !ctl.fail; ++j, ++g) {
                     const int slot = slots.slot(j), R = slots.bucket(j), s = (int)(g % GS);
                     if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
                     // columns past d_out read as zeros
-                    if (leader) mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)R * PN * 2);
-                    tma_load_4d_pair(ring + s * S::STAGE, &p.b_map[bucket_index(R)], 0, nc / p.b_col_div, 0, slot,
-                                     leader_bar(&ctl.full[s]));
+                    if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * NSUB * (uint32_t)R * PH * 2);
+#pragma unroll
+                    for (int u = 0; u < NSUB; ++u)
+                        tma_load_4d_pair(ring + s * S::STAGE + u * PH * RK * 2, &p.b_map[bucket_index(R)], 0,
+                                         (nc + u * UN) / p.b_col_div, 0, slot, leader_bar(&ctl.full[s]));
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == 2) {
+        if (lane == 0) {
+            uint32_t g = 0;
+            for (int t = first; t < n_tiles && !ctl.fail; t += n_clusters) {
+                int mb, nb;
+                tile_at(p, t, mb, nb);
+                const int stages = nkb + slot_list<RK>(sl, mb).count;
+                for (int kb = 0; kb < stages; ++kb, ++g) {
+                    const int s = (int)(g % GS);
+                    // (B chunks too: a waiter that skipped phases could not tell them apart by parity)
+                    if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+                    if (kb >= nkb) {
+                        if (leader) mbar_arrive(&ctl.full[s]);
+                        continue;
+                    }
+                    // blocks past the last read as zeros
+                    uint8_t *st = ring + s * S::STAGE + SF_AT;
+                    if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * S::NSF * SF_BYTES);
+                    const uint32_t fb = leader_bar(&ctl.full[s]);
+                    tma_load_2d_pair(st, &p.xs_map, kb * 256, 2 * mb + crank, fb);
+                    tma_load_2d_pair(st + SF_BYTES, &p.ws_map, kb * 256, nb * (PN / 128), fb);
                 }
             }
         }
@@ -719,19 +739,24 @@ __global__ void __launch_bounds__(PT, 1)
                     tc_fence_after();
                     const uint64_t xd = x0 + (uint32_t)s * (S::STAGE >> 4);   // (the address field, in 16 bytes)
                     const uint64_t wd = xd + (OP_BYTES >> 4);
-                    // per 128 of K: X's four columns of scales, then each sub-tile's (32 rows a column)
+                    // per 128 of K: X's four columns of scales, then W's (32 rows a column).  The stage's own:
+                    // their last readers finished before it was refilled
                     const uint32_t sf = tmem + PN + S::SF_COLS * s;
+                    const uint32_t sm = smem_addr(ring) + (uint32_t)s * S::STAGE + SF_AT;
                     const int steps = min(4, (p.d_in - kb * KB + 63) / 64);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint32_t sx = sf + h * 4 * S::NSF, sw = sx + 4;
                         if (issuer) {
 #pragma unroll
+                            for (int i = 0; i < S::NSF; ++i)
+                                tmem_copy_scales<2>(sx + 4 * i, sm + i * SF_BYTES + h * 512);
+#pragma unroll
                             for (int k = 2 * h; k < 2 * h + 2; ++k) {
                                 if (k >= steps) continue;
 #pragma unroll
                                 for (int u = 0; u < NSUB; ++u)
-                                    umma_mxf4<2>(tmem + u * UN, xd + 2 * k, wd + u * (PH * 128 >> 4) + 2 * k,
+                                    umma_mxf4<2>(tmem + u * UN, xd + 2 * k, wd + u * (S::W_BYTES >> 4) + 2 * k,
                                                  umma_idesc_mxf4(2 * MR, UN, (k & 1) * 2, (k & 1) * 2), sx,
                                                  sw + u * UN / 32, kb > 0 || k > 0 ? 1u : 0u);
                             }
@@ -761,11 +786,11 @@ __global__ void __launch_bounds__(PT, 1)
                             const uint32_t a_hi = smem_addr(hop + hb * 2 * HOP), a_lo = a_hi + HOP;
 #pragma unroll
                             for (int u = 0; u < NSUB; ++u) {
-                                const uint32_t b_s = smem_addr(ring + s * S::STAGE) + u * PH * 16;
+                                const uint32_t b_s = smem_addr(ring + s * S::STAGE + u * PH * RK * 2);
                                 for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
-                                    const uint32_t b0 = b_s + st * PN * 16;
+                                    const uint32_t b0 = b_s + st * 2 * PH * 16;
                                     // bucket 8: the second rank group of B is the zero block
-                                    const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PN / 2 * 16;
+                                    const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PH * 16;
                                     const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
                                     const uint32_t koff = st * 2 * (MR / 8) * 128;
                                     umma_bf16_pair(tmem + u * UN, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd,
@@ -785,79 +810,8 @@ __global__ void __launch_bounds__(PT, 1)
             }
         }
         __syncwarp();
-    } else if (warp < 10) {
-        const uint32_t group = (uint32_t)(warp - 2) >> 2;
-        const uint32_t lanes = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + PN;
-        uint32_t g = 0;
-        bool alive = true;
-        for (int t = first; t < n_tiles && alive; t += n_clusters) {
-            int mb, nb;
-            tile_at(p, t, mb, nb);
-            const int stages = nkb + slot_list<RK>(sl, mb).count;
-            for (int kb = 0; kb < stages; ++kb, ++g) {
-                const int s = (int)(g % GS);
-                if ((g & 1) != group) continue;
-                // (the products that last read these columns finished before the scales were fetched)
-                alive = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.local[s], (g / GS) & 1u));
-                if (!alive) break;
-                if (kb >= nkb) {   // a B chunk has no scales
-                    if (lane == 0) mbar_arrive_cluster(leader_bar(&ctl.full[s]));
-                    continue;
-                }
-                const uint8_t *src = ring + s * S::STAGE + SF_AT + lane * 16;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t w[4 * S::NSF];   // four 32-row groups of each block
-#pragma unroll
-                    for (int i = 0; i < S::NSF; ++i) {
-                        const uint4 v = *reinterpret_cast<const uint4 *>(src + i * SF_BYTES + h * 512);
-                        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
-                    }
-                    const uint32_t at = lanes + S::SF_COLS * s + 4 * S::NSF * h;
-                    if constexpr (NSUB == 1) {
-                        const uint32_t a[4] = {w[0], w[1], w[2], w[3]};
-                        const uint32_t b[8] = {w[4], w[5], w[6], w[7], w[8], w[9], w[10], w[11]};
-                        tmem_st4(at, a);
-                        tmem_st8(at + 4, b);
-                    } else {   // W's groups 0-2, 6-8 are sub-tile 0's columns, 3-5, 9-11 sub-tile 1's
-                        const uint32_t a[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[10]};
-                        const uint32_t b[8] = {w[11], w[12], w[7], w[8], w[9], w[13], w[14], w[15]};
-                        tmem_st8(at, a);
-                        tmem_st8(at + 8, b);
-                    }
-                }
-                tmem_wait_st();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(leader_bar(&ctl.full[s]));
-            }
-        }
-    } else if (warp == 18) {
-        if (lane == 0) {
-            uint32_t g = 0;
-            for (int t = first; t < n_tiles && !ctl.fail; t += n_clusters) {
-                int mb, nb;
-                tile_at(p, t, mb, nb);
-                const int stages = nkb + slot_list<RK>(sl, mb).count;
-                for (int kb = 0; kb < stages; ++kb, ++g) {
-                    const int s = (int)(g % GS);
-                    // (B chunks too: a waiter that skipped phases could not tell them apart by parity)
-                    if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
-                    if (kb >= nkb) {
-                        mbar_arrive(&ctl.local[s]);
-                        continue;
-                    }
-                    // blocks past the last read as zeros
-                    uint8_t *st = ring + s * S::STAGE + SF_AT;
-                    mbar_arrive_expect_tx(&ctl.local[s], S::NSF * SF_BYTES);
-                    tma_load_2d(st, &p.xs_map, kb * 256, 2 * mb + crank, &ctl.local[s]);
-                    tma_load_2d(st + SF_BYTES, &p.ws_map, kb * 256, nb * (PN / 128), &ctl.local[s]);
-                }
-            }
-        }
-        __syncwarp();
-    } else {
-        const int quarter = warp & 3, half = (warp - 10) >> 2;
+    } else if (warp >= 4) {
+        const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t empty_bar = leader_bar(&ctl.acc_empty);
         const uint32_t hop_bar0 = leader_bar(&ctl.hop_full[0]), hop_bar1 = leader_bar(&ctl.hop_full[1]);
         const int r = 32 * quarter + lane, k = lane & 7;
@@ -890,14 +844,12 @@ __global__ void __launch_bounds__(PT, 1)
                     else dirty0 = mine;
                     fence_proxy_async_smem();
                     named_sync(kEpiBar, 256);
-                    if (warp == 10 && lane == 0) mbar_arrive_cluster(hb ? hop_bar1 : hop_bar0);
+                    if (warp == 4 && lane == 0) mbar_arrive_cluster(hb ? hop_bar1 : hop_bar0);
                 }
             }
             if (!named_sync_and(kEpiBar, 256, alive && pwait(p, ctl, &ctl.acc_full, tc & 1u))) break;
             tc_fence_after();
-            // accumulator column n of sub-tile u is column PH u + n of the tile, PN / 2 - PH more from
-            // n = PH on; with one sub-tile each half of the warps has half of its columns
-            const int n0 = nb * PN + (NSUB == 1 ? HC * half : PH * half), jump = NSUB == 1 ? HC : PH;
+            const int n0 = nb * PN + HC * half;
             const int row0 = row - lane + 8 * (lane >> 3);
             const uint32_t tb = tmem + ((uint32_t)(32 * quarter) << 16) + HC * half;
             if constexpr (YT == 2) {
@@ -915,25 +867,18 @@ __global__ void __launch_bounds__(PT, 1)
                         float f[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * q + i]);
-                        const int n = c + 8 * q, col = n0 + (n < jump ? n : n + PN / 2 - PH);
-                        if (row < p.n_rows && col < p.d_out) store8<2>(p, row, col, f);
+                        if (row < p.n_rows && n0 + c + 8 * q < p.d_out) store8<2>(p, row, n0 + c + 8 * q, f);
                     }
                 }
             } else {
-                // two pieces of 64 columns fit the registers; a third is stored first
-                if constexpr (HC == 192) {
-                    uint4 a[8];
-                    take64<YT>(tb + 128, a);
-                    put64(p, a, row0, n0, 128 + 8 * k, jump, PN / 2 - PH, k);
-                }
-                uint4 a[2][8];
-                take64<YT>(tb, a[0]);
-                take64<YT>(tb + 64, a[1]);
+                uint4 a[HC / 64][8];
+#pragma unroll
+                for (int h = 0; h < HC / 64; ++h) take64<YT>(tb + 64 * h, a[h]);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive_cluster(empty_bar);
-                put64(p, a[0], row0, n0, 8 * k, jump, PN / 2 - PH, k);
-                put64(p, a[1], row0, n0, 64 + 8 * k, jump, PN / 2 - PH, k);
+#pragma unroll
+                for (int h = 0; h < HC / 64; ++h) put64(p, a[h], row0, n0 + 64 * h, k);
             }
         }
     }
@@ -1053,26 +998,30 @@ cudaError_t launch_pair(const MxGemmParams &p, const MxSlots &sl, int cols, unsi
 
 MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
 {
-    // Time of each form in units of one K block of a 128 x 128 tile on one SM: waves of
-    // resident CTAs times (K blocks per CTA + what a tile costs beside them).  A pair tile's K
-    // block is two of those units of tensor-core work per SM.
+    // Each form's time in us, as measured on a B200 with 148 SMs (shapes of 1 to 4096 rows, d_in
+    // 1024 to 14336): waves of resident CTAs or pairs times (what a tile costs + its K blocks), and
+    // for a split tile the exchange of its parts.  E.g. 256 x 4096 -> 4096: 8.4 us with one CTA a
+    // tile, 9.9 with two, 10.8 on pairs; 512 x 4096 -> 14336: 32.5, 63, 18.9; one row of
+    // 4096 -> 4096: 8.0 with one, 7.3 with two or four.
     const int64_t nkb = (d_in + KB - 1) / KB;
-    const int64_t tiles = (int64_t)((n_rows + 127) / 128) * ((d_out + MC - 1) / MC);
-    MxPlan plan{128, MC, 1};
-    int64_t best = INT64_MAX;
+    const int64_t tiles = (int64_t)((n_rows + MR - 1) / MR) * ((d_out + MC - 1) / MC);
+    MxPlan plan{MR, MC, 1};
+    double best = 1e30;
     for (int ks = 1; ks <= 8 && ks <= nkb; ks *= 2) {
-        const int64_t cost = (tiles * ks + 147) / 148 * ((nkb + ks - 1) / ks + 4) + (ks > 1 ? 2 : 0);
+        const double exchange = ks > 1 ? 1.0 + 0.5 * ks + 0.02 * std::min(n_rows, MR) : 0.0;
+        const double cost = (double)((tiles * ks + 147) / 148) * (3.1 + 0.31 * (double)((nkb + ks - 1) / ks) + exchange);
         if (cost < best) {
             best = cost;
             plan.ksplit = ks;
         }
     }
     for (int cols = 256; cols <= 384; cols += 128) {
-        const int64_t pairs = (int64_t)((n_rows + 255) / 256) * ((d_out + cols - 1) / cols);
-        const int64_t cost = (pairs + 73) / 74 * (cols / 128 * nkb + 2) + 6;
+        const int64_t pairs = (int64_t)((n_rows + 2 * MR - 1) / (2 * MR)) * ((d_out + cols - 1) / cols);
+        const double tile = cols == 256 ? 2.2 + 0.3125 * (double)nkb : 2.8 + 0.43 * (double)nkb;
+        const double cost = 3.9 + (double)((pairs + 73) / 74) * tile;
         if (cost < best) {
             best = cost;
-            plan = MxPlan{256, cols, 1};
+            plan = MxPlan{2 * MR, cols, 1};
         }
     }
     return plan;
