@@ -86,7 +86,9 @@ __device__ __forceinline__ void store8(const MxGemmParams &p, int row, int col, 
 //              tensor-memory columns and issues the products; the low-rank products have an
 //              accumulator of their own
 //   warps 2-5  find the tile's rows in the segments and its distinct slots (while the K blocks
-//              stream: no launch of its own), offer the rows' s H slot by slot, then the epilogue
+//              stream: no launch of its own), stage the rows' s H, then the epilogue
+// The low-rank operand is every row's own s H; the products of one slot's B write the lanes of
+// that slot's rows alone (the others are masked), so that it is staged once however many slots.
 // With more than one CTA each leaves its fp32 part in shared memory; after a cluster
 // barrier every CTA sums a share of the columns over the cluster in CTA order.
 namespace {
@@ -103,24 +105,28 @@ constexpr int RED_PITCH = MC + 4;          // floats per row of the reduction bu
 template <int RK>
 struct TileShape {
     static constexpr int HOP = MR * RK * 2;            // one of hi / lo
-    static constexpr int GS = RK == 64 ? 4 : 6;        // ring stages
+    static constexpr int GS = RK == 64 ? 5 : 6;        // ring stages
     static constexpr int ZERO = RK ? 2048 : 0;         // the zero second half of a rank-8 B chunk
-    static constexpr int SMEM = 1024 + GS * STAGE + 4 * HOP + ZERO;
-    static_assert(SMEM + 4096 <= 227 * 1024, "shared memory");
+    static constexpr int B_BYTES = MC * RK * 2;        // a slot's chunk of B
+    static constexpr int SLOTS = RK ? STAGE / B_BYTES : 1;   // slots per ring stage
+    static constexpr int SMEM = 1024 + GS * STAGE + 2 * HOP + ZERO;
+    static_assert(SMEM + 6144 <= 227 * 1024, "shared memory");
     static_assert(MR * RED_PITCH * 4 <= GS * STAGE, "the reduction buffer reuses the ring");
     static_assert(GS <= kMaxStages && T_SCALES + 16 * GS <= T_COLS, "tensor memory");
-    static_assert(STAGE % 1024 == 0 && MC * RK * 2 <= STAGE, "stage layout");
+    static_assert(STAGE % 1024 == 0 && SLOTS >= 1, "stage layout");
 };
 
 struct TileCtl {
     uint64_t full[kMaxStages], empty[kMaxStages];
     uint64_t done;                 // every product of the tile is in tensor memory
-    uint64_t hop_full[2], hop_empty[2];
+    uint64_t staged;               // the rows' s H are in place, the low-rank accumulator is zero
     uint64_t listed;               // the slot list is complete
     uint32_t tmem;
     volatile int fail;
     int count;                     // distinct slots of the tile's rows, and their
-    int slot[MR], bucket[MR];      // numbers and rank buckets
+    alignas(16) int slot[MR];      // numbers,
+    int bucket[MR];                // rank buckets
+    uint32_t others[MR][4];        // and, a bit each, the rows of other slots
     int pos[MR];                   // each row's grouped position (-1: none)
     alignas(16) int row_slot[MR];  // and slot
     int part[4];
@@ -193,6 +199,10 @@ __device__ int4 find_rows(const TileParams &t, TileCtl &ctl, int m0, int r, bool
         ctl.bucket[i] = rank_bucket(info.w);
     }
     if (r == 0) ctl.count = total;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) ctl.others[r][i] = 0xffffffffu;
+    named_sync(kRowBar, 128);
+    if (info.x >= 0) atomicAnd(&ctl.others[slot_index(ctl.slot, info.y)][warp], ~(1u << lane));
     named_sync(kRowBar, 128);
     return info;
 }
@@ -208,8 +218,8 @@ __global__ void __launch_bounds__(MT, 1)
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ TileCtl ctl;
     uint8_t *ring = align_1024(smem_raw);
-    uint8_t *hop = ring + GS * STAGE;              // [2][hi, lo]
-    uint8_t *zero = hop + 4 * HOP;
+    uint8_t *hop = ring + GS * STAGE;              // s H: hi, lo
+    uint8_t *zero = hop + 2 * HOP;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int ksplit = (int)cluster_size(), crank = (int)cluster_rank();
     const int tile = (int)blockIdx.x / ksplit;
@@ -226,18 +236,14 @@ __global__ void __launch_bounds__(MT, 1)
             mbar_init(&ctl.empty[s], 1);
         }
         mbar_init(&ctl.done, 1);
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&ctl.hop_full[b], 1);
-            mbar_init(&ctl.hop_empty[b], 1);
-        }
+        mbar_init(&ctl.staged, 1);
         mbar_init(&ctl.listed, 1);
         fence_mbar_init();
         ctl.fail = 0;
         ctl.count = 0;
     }
     if (RK > 0) {
-        for (int i = tid; i < (4 * HOP + S::ZERO) / 16; i += MT)
-            reinterpret_cast<uint4 *>(hop)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < S::ZERO / 16; i += MT) reinterpret_cast<uint4 *>(zero)[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
     tc_fence_before();
@@ -250,11 +256,15 @@ __global__ void __launch_bounds__(MT, 1)
     const int kb0 = nkb * crank / ksplit, kb1 = nkb * (crank + 1) / ksplit;
 
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t g = 0;
-            for (int kb = kb0; kb < kb1; ++kb, ++g) {
-                const int s = (int)(g % GS);
-                if (g >= GS && !mwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+        // (the whole warp walks the stages, one lane issues: see warp 1)
+        const bool issuer = elect_one();
+        uint32_t g = 0;
+        bool ok = true;
+        for (int kb = kb0; kb < kb1; ++kb, ++g) {
+            const int s = (int)(g % GS);
+            ok = g < GS || __all_sync(0xffffffffu, mwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u));
+            if (!ok) break;
+            if (issuer) {
                 uint8_t *st = ring + s * STAGE;
                 mbar_arrive_expect_tx(&ctl.full[s], STAGE);
                 tma_load_2d(st + OP_BYTES, &p.w_map, kb * (KB / 2), n0, &ctl.full[s]);
@@ -262,24 +272,34 @@ __global__ void __launch_bounds__(MT, 1)
                 tma_load_2d(st + 2 * OP_BYTES, &p.xs_map, kb * 256, mb, &ctl.full[s]);
                 tma_load_2d(st + 2 * OP_BYTES + SF_BYTES, &p.ws_map, kb * 256, nb, &ctl.full[s]);
             }
-            if (RK > 0 && mwait(p, ctl, &ctl.listed, 0)) {
-                const int cnt = ctl.count;
-                for (int j = crank; j < cnt; j += ksplit, ++g) {
-                    const int R = ctl.bucket[j], s = (int)(g % GS);
-                    if (g >= GS && !mwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+            __syncwarp();
+        }
+        if (RK > 0 && ok && __all_sync(0xffffffffu, mwait(p, ctl, &ctl.listed, 0))) {
+            const int mine = (ctl.count - crank + ksplit - 1) / ksplit;   // slots crank, + ksplit, ...
+            for (int i0 = 0; i0 < mine; i0 += S::SLOTS, ++g) {
+                const int s = (int)(g % GS), n = min(S::SLOTS, mine - i0);
+                if (g >= GS && !__all_sync(0xffffffffu, mwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u))) break;
+                if (issuer) {
+                    int ranks = 0;
+                    for (int i = 0; i < n; ++i) ranks += ctl.bucket[crank + (i0 + i) * ksplit];
                     // columns past d_out read as zeros
-                    mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)R * MC * 2);
-                    tma_load_4d(ring + s * STAGE, &p.b_map[bucket_index(R)], 0, n0 / p.b_col_div, 0, ctl.slot[j],
-                                &ctl.full[s]);
+                    mbar_arrive_expect_tx(&ctl.full[s], (uint32_t)ranks * MC * 2);
+                    for (int i = 0; i < n; ++i) {
+                        const int j = crank + (i0 + i) * ksplit;
+                        tma_load_4d(ring + s * STAGE + i * S::B_BYTES, &p.b_map[bucket_index(ctl.bucket[j])], 0,
+                                    n0 / p.b_col_div, 0, ctl.slot[j], &ctl.full[s]);
+                    }
                 }
+                __syncwarp();
             }
         }
-        __syncwarp();
     } else if (warp == 1) {
-        // (as in the pair kernel: the whole warp walks the stages, one lane issues)
+        // The whole warp walks the stages, one lane of it issues: the descriptors then live in uniform
+        // registers, where the products take them from.  (A lone lane spent about 110 cycles a
+        // product on moving them there: a K block took 0.66 us instead of 0.33.)
         const bool issuer = elect_one();
         const uint64_t x0 = umma_desc_sw128(smem_addr(ring));
-        uint32_t g = 0, hc = 0;
+        uint32_t g = 0;
         bool ok = true;
         for (int kb = kb0; kb < kb1; ++kb, ++g) {
             const int s = (int)(g % GS);
@@ -308,32 +328,36 @@ __global__ void __launch_bounds__(MT, 1)
             __syncwarp();
         }
         if (RK > 0 && ok) ok = __all_sync(0xffffffffu, mwait(p, ctl, &ctl.listed, 0));
-        if (RK > 0 && ok) {
+        if (RK > 0 && ok && ctl.count > crank) {
+            ok = __all_sync(0xffffffffu, mwait(p, ctl, &ctl.staged, 0));
             constexpr uint32_t idesc = umma_idesc_bf16(MR, MC);
-            const int cnt = ctl.count;
-            for (int j = crank; j < cnt; j += ksplit, ++g, ++hc) {
-                const int R = ctl.bucket[j];
-                const int s = (int)(g % GS), hb = (int)(hc & 1);
-                ok = __all_sync(0xffffffffu, mwait(p, ctl, &ctl.hop_full[hb], (hc >> 1) & 1u) &&
-                                                 mwait(p, ctl, &ctl.full[s], (g / GS) & 1u));
+            const int mine = (ctl.count - crank + ksplit - 1) / ksplit;
+            const uint32_t a_hi = smem_addr(hop), a_lo = a_hi + HOP;
+            for (int i0 = 0; i0 < mine && ok; i0 += S::SLOTS, ++g) {
+                const int s = (int)(g % GS), n = min(S::SLOTS, mine - i0);
+                ok = __all_sync(0xffffffffu, mwait(p, ctl, &ctl.full[s], (g / GS) & 1u));
                 if (!ok) break;
                 tc_fence_after();
-                if (issuer) {
-                    const uint32_t a_hi = smem_addr(hop + hb * 2 * HOP), a_lo = a_hi + HOP;
-                    const uint32_t b_s = smem_addr(ring + s * STAGE);
-                    for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
-                        const uint32_t b0 = b_s + st * 2 * MC * 16;
-                        // bucket 8: the second rank group of B is the zero block
-                        const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : MC * 16;
-                        const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
-                        const uint32_t koff = st * 2 * (MR / 8) * 128;
-                        umma_bf16(tmem + T_LORA, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd, idesc,
-                                  hc > 0 || st > 0 ? 1u : 0u);
-                        umma_bf16(tmem + T_LORA, umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd, idesc, 1u);
+                for (int i = 0; i < n; ++i) {
+                    const int j = crank + (i0 + i) * ksplit, R = ctl.bucket[j];
+                    const uint4 others = *reinterpret_cast<const uint4 *>(ctl.others[j]);
+                    const uint32_t b_s = smem_addr(ring) + (uint32_t)(s * STAGE + i * S::B_BYTES);
+                    if (issuer) {
+                        for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
+                            const uint32_t b0 = b_s + st * 2 * MC * 16;
+                            // bucket 8: the second rank group of B is the zero block
+                            const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : MC * 16;
+                            const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
+                            const uint32_t koff = st * 2 * (MR / 8) * 128;
+                            umma_bf16_rows(tmem + T_LORA, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd, idesc,
+                                           others);
+                            umma_bf16_rows(tmem + T_LORA, umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd, idesc,
+                                           others);
+                        }
                     }
-                    umma_commit(&ctl.empty[s]);
-                    umma_commit(&ctl.hop_empty[hb]);
+                    __syncwarp();
                 }
+                if (issuer) umma_commit(&ctl.empty[s]);
                 __syncwarp();
             }
         }
@@ -341,32 +365,29 @@ __global__ void __launch_bounds__(MT, 1)
         __syncwarp();
     } else {
         const int r = tid - 64, quarter = warp & 3;
-        bool alive = true, lora = false;
+        bool lora = false;
         if constexpr (RK > 0) {
             const int4 info = find_rows(sg.t, ctl, m0, r, blockIdx.x == 0);
             if (r == 0) mbar_arrive(&ctl.listed);
-            const int cnt = ctl.count;
-            lora = cnt > crank;   // this CTA has a slot
-            RowOperand<RK, 1> op;
-            if (info.x >= 0) op.load(sg.H + (int64_t)info.x * sg.ldh, info.w, __int_as_float(info.z), 0);
-            bool dirty0 = false, dirty1 = false;   // this row of the buffer holds values
-            uint32_t hc = 0;
-            for (int j = crank; j < cnt; j += ksplit, ++hc) {
-                const int hb = (int)(hc & 1);
-                if (hc >= 2 && !named_sync_and(kRowBar, 128, mwait(p, ctl, &ctl.hop_empty[hb], ((hc >> 1) - 1) & 1u))) {
-                    alive = false;
-                    break;
+            lora = ctl.count > crank;   // this CTA has a slot
+            if (lora) {
+                if (info.x >= 0) {
+                    RowOperand<RK, 1> op;
+                    op.load(sg.H + (int64_t)info.x * sg.ldh, info.w, __int_as_float(info.z), 0);
+                    op.store(hop, r, 0);
                 }
-                const bool mine = info.x >= 0 && info.y == ctl.slot[j];
-                if (mine || (hb ? dirty1 : dirty0)) op.store(hop + hb * 2 * HOP, r, 0, mine);
-                if (hb) dirty1 = mine;
-                else dirty0 = mine;
+                // the low-rank accumulator starts at zero: no product writes all of its rows
+                const uint32_t none[8] = {};
+                for (int c = 0; c < MC; c += 8)
+                    tmem_st8(tmem + ((uint32_t)(32 * quarter) << 16) + T_LORA + c, none);
+                tmem_wait_st();
+                tc_fence_before();
                 fence_proxy_async_smem();
                 named_sync(kRowBar, 128);
-                if (r == 0) mbar_arrive(&ctl.hop_full[hb]);
+                if (r == 0) mbar_arrive(&ctl.staged);
             }
         }
-        alive = named_sync_and(kRowBar, 128, alive && mwait(p, ctl, &ctl.done, 0));
+        const bool alive = named_sync_and(kRowBar, 128, mwait(p, ctl, &ctl.done, 0));
         if (alive) {
             tc_fence_after();
             const int row = m0 + 32 * quarter + lane;
@@ -449,8 +470,9 @@ __global__ void __launch_bounds__(MT, 1)
 //   warp 1     even CTA: copies a stage's scales into that stage's own columns of tensor memory
 //              and issues the pair's products; after the K blocks it waits for them before the
 //              low-rank products, whose instruction kind differs, continue the same accumulator
-//   warps 4-11 offer the rows' s H slot by slot, then the epilogue: quarter = warp % 4 of the
-//              rows, half = (warp - 4) / 4 of the ranks and of the columns
+//   warps 4-11 stage the rows' s H, the tile's slots and their rows' masks while the K blocks run,
+//              then the epilogue: quarter = warp % 4 of the rows, half = (warp - 4) / 4 of the
+//              ranks and of the columns
 namespace {
 
 constexpr int PT = 12 * 32;
@@ -469,13 +491,13 @@ struct PairShape {
     static constexpr int SF_COLS = 8 * NSF;            // their columns of tensor memory
     static constexpr int STAGE = OP_BYTES + NSUB * W_BYTES + (NSF * SF_BYTES + 1023) / 1024 * 1024;
     static constexpr int HOP = MR * RK * 2;
-    static constexpr int HB = RK == 64 ? 1 : 2;        // operand buffers
     static constexpr int GS = NSUB == 2 ? 4 : RK ? 5 : 6;   // ring stages
     static constexpr int ZERO = RK ? 2048 : 0;
-    static constexpr int SMEM = 1024 + GS * STAGE + HB * 2 * HOP + ZERO;
-    static_assert(SMEM + 1024 <= 227 * 1024, "shared memory");
+    static constexpr int B_BYTES = NSUB * PH * RK * 2; // a slot's chunk of B
+    static constexpr int SLOTS = RK ? STAGE / B_BYTES : 1;   // slots per ring stage
+    static constexpr int SMEM = 1024 + GS * STAGE + 2 * HOP + ZERO;
     static_assert(PN + SF_COLS * GS <= P_COLS && GS <= kPairStages, "tensor memory");
-    static_assert(STAGE % 1024 == 0 && NSUB * PH * RK * 2 <= STAGE, "stage layout");
+    static_assert(STAGE % 1024 == 0 && SLOTS >= 1, "stage layout");
 };
 
 struct PairCtl {
@@ -484,9 +506,13 @@ struct PairCtl {
     uint64_t empty[kPairStages];   // the products are done
     uint64_t acc_full, acc_empty;
     uint64_t k_done;               // the K blocks' products are complete
-    uint64_t hop_full[2], hop_empty[2];
+    uint64_t listed;               // the tile's slots are in this CTA's list,
+    uint64_t staged;               // the rows' s H in both CTAs' shared memory
     uint32_t tmem;
     volatile int fail;
+    alignas(16) int slot[2 * MR];  // a tile's distinct slots, their
+    int bucket[2 * MR];            // rank buckets,
+    uint32_t others[2 * MR][8];    // and, a bit each, the rows of other slots (the issuing CTA's)
 };
 
 // Bounded wait.  The flag of a wait that ran out, here or in the pair's other CTA (which is
@@ -519,28 +545,11 @@ __device__ __forceinline__ void tile_at(const MxGemmParams &p, int t, int &mb, i
     nb = local / rows;
 }
 
-// A row block's distinct slots.  The count and the first two are read at once, when a tile
-// begins: after its K blocks their latency would be the tile's.
-struct SlotList {
-    const int32_t *list;
-    int count, slot0, bucket0, slot1, bucket1;
-    __device__ __forceinline__ int slot(int j) const { return j == 0 ? slot0 : j == 1 ? slot1 : list[1 + 2 * j]; }
-    __device__ __forceinline__ int bucket(int j) const { return j == 0 ? bucket0 : j == 1 ? bucket1 : list[2 + 2 * j]; }
-};
-
+// Distinct slots of a row block.
 template <int RK>
-__device__ __forceinline__ SlotList slot_list(const MxSlots &sl, int mb)
+__device__ __forceinline__ int slot_count(const MxSlots &sl, int mb)
 {
-    SlotList s{};
-    if constexpr (RK > 0) {
-        s.list = sl.block_slots + (int64_t)mb * kBlockSlotsPitch;
-        s.count = s.list[0];
-        s.slot0 = s.list[1];
-        s.bucket0 = s.list[2];
-        s.slot1 = s.list[3];
-        s.bucket1 = s.list[4];
-    }
-    return s;
+    return RK > 0 ? sl.block_slots[(int64_t)mb * kBlockSlotsPitch] : 0;
 }
 
 __device__ __forceinline__ uint32_t leader_bar(const uint64_t *bar) { return map_to_rank(smem_addr(bar), 0); }
@@ -609,13 +618,14 @@ __global__ void __launch_bounds__(PT, 1)
     mx_pair_kernel(const __grid_constant__ MxGemmParams p, const __grid_constant__ MxSlots sl)
 {
     using S = PairShape<RK, NSUB>;
-    constexpr int GS = S::GS, HOP = S::HOP, HB = S::HB, UN = S::UN, PN = S::PN, PH = S::PH;
+    constexpr int GS = S::GS, HOP = S::HOP, UN = S::UN, PN = S::PN, PH = S::PH, SLOTS = S::SLOTS;
+    static_assert(S::SMEM + sizeof(PairCtl) <= 227 * 1024, "shared memory");
     constexpr int SF_AT = OP_BYTES + NSUB * S::W_BYTES;   // scales in a stage: X's block, then W's
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ PairCtl ctl;
     uint8_t *ring = align_1024(smem_raw);
-    uint8_t *hop = ring + GS * S::STAGE;           // [HB][hi, lo]
-    uint8_t *zero = hop + HB * 2 * HOP;
+    uint8_t *hop = ring + GS * S::STAGE;           // s H: hi, lo
+    uint8_t *zero = hop + 2 * HOP;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int crank = (int)cluster_rank();         // 0 issues the pair's products
     const bool leader = crank == 0;
@@ -633,16 +643,13 @@ __global__ void __launch_bounds__(PT, 1)
         mbar_init(&ctl.acc_full, 1);
         mbar_init(&ctl.acc_empty, 16);             // eight epilogue warps in each CTA
         mbar_init(&ctl.k_done, 1);
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&ctl.hop_full[b], 2);        // one arrival per CTA
-            mbar_init(&ctl.hop_empty[b], 1);
-        }
+        mbar_init(&ctl.listed, 1);
+        mbar_init(&ctl.staged, 2);                 // one arrival per CTA
         fence_mbar_init();
         ctl.fail = 0;
     }
     if (RK > 0) {
-        for (int i = tid; i < (HB * 2 * HOP + S::ZERO) / 16; i += PT)
-            reinterpret_cast<uint4 *>(hop)[i] = make_uint4(0, 0, 0, 0);
+        for (int i = tid; i < S::ZERO / 16; i += PT) reinterpret_cast<uint4 *>(zero)[i] = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
     }
     tc_fence_before();
@@ -657,18 +664,22 @@ __global__ void __launch_bounds__(PT, 1)
     const int n_tiles = p.n_mblk * p.n_nblk;
     const int nkb = (p.d_in + KB - 1) / KB;
 
-    // Ring stages are counted by g: a tile's K blocks, then its slots' B chunks.
+    // Ring stages are counted by g: a tile's K blocks, then its slots' B chunks, SLOTS to a stage.
+    // The warps that issue walk them whole, one lane issues: see mx_tile_kernel.
     if (warp == 0) {
-        if (lane == 0) {
-            uint32_t g = 0;
-            for (int t = first; t < n_tiles && !ctl.fail; t += n_clusters) {
-                int mb, nb;
-                tile_at(p, t, mb, nb);
-                const SlotList slots = slot_list<RK>(sl, mb);
-                const int m0 = (2 * mb + crank) * MR, nc = nb * PN + PH * crank;
-                for (int kb = 0; kb < nkb; ++kb, ++g) {
-                    const int s = (int)(g % GS);
-                    if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+        const bool issuer = elect_one();
+        uint32_t g = 0, lc = 0;
+        bool ok = true;
+        for (int t = first; t < n_tiles && ok; t += n_clusters) {
+            int mb, nb;
+            tile_at(p, t, mb, nb);
+            const int count = slot_count<RK>(sl, mb);   // (used after the K blocks)
+            const int m0 = (2 * mb + crank) * MR, nc = nb * PN + PH * crank;
+            for (int kb = 0; kb < nkb; ++kb, ++g) {
+                const int s = (int)(g % GS);
+                ok = g < GS || __all_sync(0xffffffffu, pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u));
+                if (!ok) break;
+                if (issuer) {
                     uint8_t *st = ring + s * S::STAGE;
                     if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * SF_AT);
                     const uint32_t fb = leader_bar(&ctl.full[s]);
@@ -678,57 +689,69 @@ __global__ void __launch_bounds__(PT, 1)
                     for (int u = 0; u < NSUB; ++u)
                         tma_load_2d_pair(st + OP_BYTES + u * S::W_BYTES, &p.w_map, kb * (KB / 2), nc + u * UN, fb);
                 }
-                for (int j = 0; j < slots.count && !ctl.fail; ++j, ++g) {
-                    const int slot = slots.slot(j), R = slots.bucket(j), s = (int)(g % GS);
-                    if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
-                    // columns past d_out read as zeros
-                    if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * NSUB * (uint32_t)R * PH * 2);
+                __syncwarp();
+            }
+            if (RK > 0 && ok && count > 0) {
+                ok = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.listed, lc++ & 1u));
+                for (int i0 = 0; i0 < count && ok; i0 += SLOTS, ++g) {
+                    const int s = (int)(g % GS), n = min(SLOTS, count - i0);
+                    ok = g < GS || __all_sync(0xffffffffu, pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u));
+                    if (!ok) break;
+                    if (issuer) {
+                        int ranks = 0;
+                        for (int i = 0; i < n; ++i) ranks += ctl.bucket[i0 + i];
+                        // columns past d_out read as zeros
+                        if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * NSUB * (uint32_t)ranks * PH * 2);
+                        const uint32_t fb = leader_bar(&ctl.full[s]);
+                        for (int i = 0; i < n; ++i)
 #pragma unroll
-                    for (int u = 0; u < NSUB; ++u)
-                        tma_load_4d_pair(ring + s * S::STAGE + u * PH * RK * 2, &p.b_map[bucket_index(R)], 0,
-                                         (nc + u * UN) / p.b_col_div, 0, slot, leader_bar(&ctl.full[s]));
+                            for (int u = 0; u < NSUB; ++u)
+                                tma_load_4d_pair(ring + s * S::STAGE + i * S::B_BYTES + u * PH * RK * 2,
+                                                 &p.b_map[bucket_index(ctl.bucket[i0 + i])], 0,
+                                                 (nc + u * UN) / p.b_col_div, 0, ctl.slot[i0 + i], fb);
+                    }
+                    __syncwarp();
                 }
             }
         }
-        __syncwarp();
     } else if (warp == 2) {
-        if (lane == 0) {
-            uint32_t g = 0;
-            for (int t = first; t < n_tiles && !ctl.fail; t += n_clusters) {
-                int mb, nb;
-                tile_at(p, t, mb, nb);
-                const int stages = nkb + slot_list<RK>(sl, mb).count;
-                for (int kb = 0; kb < stages; ++kb, ++g) {
-                    const int s = (int)(g % GS);
-                    // (B chunks too: a waiter that skipped phases could not tell them apart by parity)
-                    if (g >= GS && !pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u)) break;
+        const bool issuer = elect_one();
+        uint32_t g = 0;
+        bool ok = true;
+        for (int t = first; t < n_tiles && ok; t += n_clusters) {
+            int mb, nb;
+            tile_at(p, t, mb, nb);
+            const int stages = nkb + (slot_count<RK>(sl, mb) + SLOTS - 1) / SLOTS;
+            for (int kb = 0; kb < stages; ++kb, ++g) {
+                const int s = (int)(g % GS);
+                // (B chunks too: a waiter that skipped phases could not tell them apart by parity)
+                ok = g < GS || __all_sync(0xffffffffu, pwait(p, ctl, &ctl.empty[s], ((g / GS) - 1) & 1u));
+                if (!ok) break;
+                if (issuer) {
                     if (kb >= nkb) {
                         if (leader) mbar_arrive(&ctl.full[s]);
-                        continue;
+                    } else {
+                        // blocks past the last read as zeros
+                        uint8_t *st = ring + s * S::STAGE + SF_AT;
+                        if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * S::NSF * SF_BYTES);
+                        const uint32_t fb = leader_bar(&ctl.full[s]);
+                        tma_load_2d_pair(st, &p.xs_map, kb * 256, 2 * mb + crank, fb);
+                        tma_load_2d_pair(st + SF_BYTES, &p.ws_map, kb * 256, nb * (PN / 128), fb);
                     }
-                    // blocks past the last read as zeros
-                    uint8_t *st = ring + s * S::STAGE + SF_AT;
-                    if (leader) mbar_arrive_expect_tx(&ctl.full[s], 2u * S::NSF * SF_BYTES);
-                    const uint32_t fb = leader_bar(&ctl.full[s]);
-                    tma_load_2d_pair(st, &p.xs_map, kb * 256, 2 * mb + crank, fb);
-                    tma_load_2d_pair(st + SF_BYTES, &p.ws_map, kb * 256, nb * (PN / 128), fb);
                 }
+                __syncwarp();
             }
         }
-        __syncwarp();
     } else if (warp == 1) {
-        // The whole warp walks the stages, one lane of it issues: the descriptors then live in uniform
-        // registers, where the products take them from (one lane alone spent about 110 cycles a
-        // product on moving them there, more than the products of a 192-column sub-tile take).
         if (leader) {
             const bool issuer = elect_one();
             const uint64_t x0 = umma_desc_sw128(smem_addr(ring));
-            uint32_t g = 0, hc = 0, tc = 0, kc = 0;
+            uint32_t g = 0, tc = 0, lc = 0;
             bool ok = true, ready = false;   // ready: the next stage was full when last looked at
             for (int t = first; t < n_tiles && ok; t += n_clusters, ++tc) {
                 int mb, nb;
                 tile_at(p, t, mb, nb);
-                const SlotList slots = slot_list<RK>(sl, mb);
+                const int count = slot_count<RK>(sl, mb);
                 if (tc > 0 && !__all_sync(0xffffffffu, pwait(p, ctl, &ctl.acc_empty, (tc - 1) & 1u))) break;
                 for (int kb = 0; kb < nkb; ++kb, ++g) {
                     const int s = (int)(g % GS);
@@ -770,38 +793,47 @@ __global__ void __launch_bounds__(PT, 1)
                     if (issuer) umma_commit_pair(&ctl.empty[s], kPairMask);
                     __syncwarp();
                 }
-                if (RK > 0 && ok && slots.count > 0) {
+                if (RK > 0 && ok && count > 0) {
                     if (issuer) umma_commit_pair(&ctl.k_done, kPairMask);
                     __syncwarp();
-                    ok = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.k_done, kc++ & 1u));
+                    ready = false;
+                    ok = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.staged, lc & 1u) &&
+                                                     pwait(p, ctl, &ctl.listed, lc & 1u) &&
+                                                     pwait(p, ctl, &ctl.k_done, lc & 1u));
+                    ++lc;
                     constexpr uint32_t idesc = umma_idesc_bf16(2 * MR, UN);
-                    for (int j = 0; j < slots.count && ok; ++j, ++g, ++hc) {
-                        const int R = slots.bucket(j), s = (int)(g % GS), hb = (int)(hc % HB);
-                        ready = false;
-                        ok = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.hop_full[hb], (hc / HB) & 1u) &&
-                                                         pwait(p, ctl, &ctl.full[s], (g / GS) & 1u));
+                    const uint32_t a_hi = smem_addr(hop), a_lo = a_hi + HOP;
+                    for (int i0 = 0; i0 < count && ok; i0 += SLOTS, ++g) {
+                        const int s = (int)(g % GS), n = min(SLOTS, count - i0);
+                        ok = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.full[s], (g / GS) & 1u));
                         if (!ok) break;
                         tc_fence_after();
-                        if (issuer) {
-                            const uint32_t a_hi = smem_addr(hop + hb * 2 * HOP), a_lo = a_hi + HOP;
+                        for (int i = 0; i < n; ++i) {
+                            const int R = ctl.bucket[i0 + i];
+                            const uint4 *others = reinterpret_cast<const uint4 *>(ctl.others[i0 + i]);
+                            const uint4 o0 = others[0], o1 = others[1];
+                            const uint32_t b_i = smem_addr(ring) + (uint32_t)(s * S::STAGE + i * S::B_BYTES);
+                            if (issuer) {
 #pragma unroll
-                            for (int u = 0; u < NSUB; ++u) {
-                                const uint32_t b_s = smem_addr(ring + s * S::STAGE + u * PH * RK * 2);
-                                for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
-                                    const uint32_t b0 = b_s + st * 2 * PH * 16;
-                                    // bucket 8: the second rank group of B is the zero block
-                                    const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PH * 16;
-                                    const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
-                                    const uint32_t koff = st * 2 * (MR / 8) * 128;
-                                    umma_bf16_pair(tmem + u * UN, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd,
-                                                   idesc, 1u);
-                                    umma_bf16_pair(tmem + u * UN, umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd,
-                                                   idesc, 1u);
+                                for (int u = 0; u < NSUB; ++u) {
+                                    for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
+                                        const uint32_t b0 = b_i + u * PH * RK * 2 + st * 2 * PH * 16;
+                                        // bucket 8: the second rank group of B is the zero block
+                                        const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PH * 16;
+                                        const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
+                                        const uint32_t koff = st * 2 * (MR / 8) * 128;
+                                        umma_bf16_rows_pair(tmem + u * UN,
+                                                            umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd,
+                                                            idesc, o0, o1);
+                                        umma_bf16_rows_pair(tmem + u * UN,
+                                                            umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd,
+                                                            idesc, o0, o1);
+                                    }
                                 }
                             }
-                            umma_commit_pair(&ctl.empty[s], kPairMask);
-                            umma_commit_pair(&ctl.hop_empty[hb], kPairMask);
+                            __syncwarp();
                         }
+                        if (issuer) umma_commit_pair(&ctl.empty[s], kPairMask);
                         __syncwarp();
                     }
                 }
@@ -813,41 +845,50 @@ __global__ void __launch_bounds__(PT, 1)
     } else if (warp >= 4) {
         const int quarter = warp & 3, half = (warp - 4) >> 2;
         const uint32_t empty_bar = leader_bar(&ctl.acc_empty);
-        const uint32_t hop_bar0 = leader_bar(&ctl.hop_full[0]), hop_bar1 = leader_bar(&ctl.hop_full[1]);
+        const uint32_t staged_bar = leader_bar(&ctl.staged);
         const int r = 32 * quarter + lane, k = lane & 7;
         constexpr int HC = PN / 2;                 // columns per thread
-        bool dirty0 = false, dirty1 = false;       // this row of an operand buffer holds values
-        uint32_t tc = 0, hc = 0;
-        bool alive = true;
-        for (int t = first; t < n_tiles && alive; t += n_clusters, ++tc) {
+        uint32_t tc = 0;
+        for (int t = first; t < n_tiles; t += n_clusters, ++tc) {
             int mb, nb;
             tile_at(p, t, mb, nb);
             const int row = (2 * mb + crank) * MR + r;
+            const int count = slot_count<RK>(sl, mb);
             if constexpr (RK > 0) {
-                // this tile's operand, while its K blocks run: this row, half of the ranks
-                const SlotList slots = slot_list<RK>(sl, mb);
-                int4 info = make_int4(-1, -1, 0, 0);
-                if (slots.count > 0 && row < p.n_rows) info = sl.row_info[row];
-                RowOperand<RK, 2> op;
-                if (info.x >= 0)
-                    op.load(sl.H + (int64_t)info.x * sl.ldh, info.w, __int_as_float(info.z), half);
-                for (int j = 0; j < slots.count; ++j, ++hc) {
-                    const int hb = (int)(hc % HB);
-                    if (hc >= HB &&
-                        !named_sync_and(kEpiBar, 256, pwait(p, ctl, &ctl.hop_empty[hb], ((hc / HB) - 1) & 1u))) {
-                        alive = false;
-                        break;
+                if (count > 0) {
+                    // This tile's operand, while its K blocks run (the last tile's products are done): this
+                    // row, half of the ranks; and the list, an entry per thread.
+                    const int i = tid - 128;
+                    int4 info = make_int4(-1, -1, 0, 0);
+                    if (row < p.n_rows) info = sl.row_info[row];
+                    int its_slot = -1;   // of the block's row i
+                    if (leader && 2 * mb * MR + i < p.n_rows) {
+                        const int4 v = sl.row_info[2 * mb * MR + i];
+                        if (v.x >= 0) its_slot = v.y;
                     }
-                    const bool mine = info.x >= 0 && info.y == slots.slot(j);
-                    if (mine || (hb ? dirty1 : dirty0)) op.store(hop + hb * 2 * HOP, r, half, mine);
-                    if (hb) dirty1 = mine;
-                    else dirty0 = mine;
+                    if (i < count) {
+                        const int32_t *entry = sl.block_slots + (int64_t)mb * kBlockSlotsPitch + 1 + 2 * i;
+                        ctl.slot[i] = entry[0];
+                        ctl.bucket[i] = entry[1];
+                        uint4 *o = reinterpret_cast<uint4 *>(ctl.others[i]);
+                        o[0] = o[1] = make_uint4(0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu);
+                    }
+                    if (info.x >= 0) {
+                        RowOperand<RK, 2> op;
+                        op.load(sl.H + (int64_t)info.x * sl.ldh, info.w, __int_as_float(info.z), half);
+                        op.store(hop, r, half);
+                    }
                     fence_proxy_async_smem();
                     named_sync(kEpiBar, 256);
-                    if (warp == 4 && lane == 0) mbar_arrive_cluster(hb ? hop_bar1 : hop_bar0);
+                    if (its_slot >= 0) atomicAnd(&ctl.others[slot_index(ctl.slot, its_slot)][i >> 5], ~(1u << (i & 31)));
+                    named_sync(kEpiBar, 256);
+                    if (i == 0) {
+                        mbar_arrive(&ctl.listed);
+                        mbar_arrive_cluster(staged_bar);
+                    }
                 }
             }
-            if (!named_sync_and(kEpiBar, 256, alive && pwait(p, ctl, &ctl.acc_full, tc & 1u))) break;
+            if (!named_sync_and(kEpiBar, 256, pwait(p, ctl, &ctl.acc_full, tc & 1u))) break;
             tc_fence_after();
             const int n0 = nb * PN + HC * half;
             const int row0 = row - lane + 8 * (lane >> 3);

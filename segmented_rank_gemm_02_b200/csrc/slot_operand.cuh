@@ -51,10 +51,8 @@ __device__ __forceinline__ void stage_operand(uint8_t *hi, uint8_t *lo, const fl
     }
 }
 
-// One row's s * H in registers, as the bf16 hi + lo parts that stage_operand writes, for kernels
-// that offer the operand slot by slot: a row belongs to one slot, so its values are loaded once
-// and written once, and the buffers are zero everywhere else.  PARTS threads share a row, each
-// RK / PARTS of the ranks.
+// One row's s * H as the bf16 hi + lo parts that stage_operand writes, zeros past its rank, for
+// kernels that stage every row's own once.  PARTS threads share a row, each RK / PARTS of the ranks.
 template <int RK, int PARTS>
 struct RowOperand {
     static constexpr int N = RK / PARTS;   // a multiple of 8
@@ -84,18 +82,17 @@ struct RowOperand {
         }
     }
 
-    // Row r of a buffer (hi, then lo): the values, or zeros.
-    __device__ __forceinline__ void store(uint8_t *buf, int r, int part, bool values) const
+    // Row r of the operand (hi, then lo).
+    __device__ __forceinline__ void store(uint8_t *buf, int r, int part) const
     {
         constexpr int HOP = kOperandRows * RK * 2;
 #pragma unroll
         for (int cg = 0; cg < N / 8; ++cg) {
             const int off = ((part * (N / 8) + cg) * (kOperandRows / 8) + r / 8) * 128 + (r % 8) * 16;
-            const uint4 z = make_uint4(0, 0, 0, 0);
             *reinterpret_cast<uint4 *>(buf + off) =
-                values ? make_uint4(hi[4 * cg], hi[4 * cg + 1], hi[4 * cg + 2], hi[4 * cg + 3]) : z;
+                make_uint4(hi[4 * cg], hi[4 * cg + 1], hi[4 * cg + 2], hi[4 * cg + 3]);
             *reinterpret_cast<uint4 *>(buf + HOP + off) =
-                values ? make_uint4(lo[4 * cg], lo[4 * cg + 1], lo[4 * cg + 2], lo[4 * cg + 3]) : z;
+                make_uint4(lo[4 * cg], lo[4 * cg + 1], lo[4 * cg + 2], lo[4 * cg + 3]);
         }
     }
 };
@@ -168,6 +165,20 @@ __device__ __forceinline__ bool first_with_slot(const int *slots, int r, int slo
         if (s.x == slot || s.y == slot || s.z == slot || s.w == slot) return false;
     }
     return true;
+}
+
+// Index of a slot in a list of distinct slots (16-byte aligned, in shared memory) that holds it.
+__device__ __forceinline__ int slot_index(const int *list, int slot)
+{
+    const int4 *v = reinterpret_cast<const int4 *>(list);
+    for (int i = 0; i < 2 * kOperandRows / 4; ++i) {
+        const int4 s = v[i];
+        if (s.x == slot) return 4 * i;
+        if (s.y == slot) return 4 * i + 1;
+        if (s.z == slot) return 4 * i + 2;
+        if (s.w == slot) return 4 * i + 3;
+    }
+    return 0;
 }
 
 }  // namespace mlora
