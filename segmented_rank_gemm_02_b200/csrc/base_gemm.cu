@@ -221,6 +221,8 @@ constexpr int kSearchThreads = 512;
 __global__ void __launch_bounds__(kSearchThreads)
     row_blocks_kernel(const __grid_constant__ TileParams p, int4 *row_info, int32_t *block_slots)
 {
+    constexpr int kRecords = 1024;
+    __shared__ int4 s_records[kRecords];
     __shared__ int s_pos[PM];
     __shared__ __align__(16) int s_slot[PM];
     __shared__ int s_count[PM / 32];
@@ -228,33 +230,13 @@ __global__ void __launch_bounds__(kSearchThreads)
     const int row0 = blockIdx.x * PM;
     const bool reporter = blockIdx.x == 0;
     if (tid < PM) s_pos[tid] = -1;
+    const SegmentTable segments = copy_segments(p, s_records, kRecords, tid, kSearchThreads, reporter);
     __syncthreads();
-    if (reporter) {
-        for (int g = tid; g < p.n_segments; g += kSearchThreads) {
-            int rank = 0;
-            float scale = 0.f;
-            const unsigned f = segment_problem(p, g, p.slots[g], p.offsets[g], p.offsets[g + 1], rank, scale);
-            if (f) atomicOr(p.status, f);
-        }
-    }
-    for (int64_t q0 = tid; q0 < p.n_tokens; q0 += 4 * kSearchThreads) {
-        int row[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int64_t q = q0 + u * kSearchThreads;
-            row[u] = q < p.n_tokens && p.token_indices ? p.token_indices[q] : (int)q;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int64_t q = q0 + u * kSearchThreads;
-            const int at = q < p.n_tokens ? claimed_row(p, (int)q, row[u], row0, PM, reporter) : -1;
-            if (at >= 0 && atomicCAS(&s_pos[at], -1, (int)q) != -1) atomicOr(p.status, kFlagBadRow);
-        }
-    }
+    claim_rows(p, segments, row0, PM, s_pos, tid, kSearchThreads, reporter);
     __syncthreads();
     int4 info = make_int4(-1, -1, 0, 0);
     if (tid < PM) {
-        if (s_pos[tid] >= 0) info = row_of_position(p, s_pos[tid]);
+        if (s_pos[tid] >= 0) info = row_of_position(p, segments, s_pos[tid]);
         if (row0 + tid < p.n_rows) row_info[row0 + tid] = info;
         s_slot[tid] = info.y;
     }

@@ -110,7 +110,7 @@ struct TileShape {
     static constexpr int B_BYTES = MC * RK * 2;        // a slot's chunk of B
     static constexpr int SLOTS = RK ? STAGE / B_BYTES : 1;   // slots per ring stage
     static constexpr int SMEM = 1024 + GS * STAGE + 2 * HOP + ZERO;
-    static_assert(SMEM + 6144 <= 227 * 1024, "shared memory");
+    static_assert(SMEM + 6144 <= 227 * 1024, "shared memory");   // and TileCtl
     static_assert(MR * RED_PITCH * 4 <= GS * STAGE, "the reduction buffer reuses the ring");
     static_assert(GS <= kMaxStages && T_SCALES + 16 * GS <= T_COLS, "tensor memory");
     static_assert(STAGE % 1024 == 0 && SLOTS >= 1, "stage layout");
@@ -151,36 +151,17 @@ __device__ __forceinline__ bool mwait(const MxGemmParams &p, TileCtl &ctl, uint6
 // The operand warps' 128 threads: row r's grouped position, slot, scale and rank (position -1:
 // base only), and the distinct slots of the tile in order of first appearance.  The first CTA
 // of the launch reports the segments' and rows' problems, as row_map_kernel does.
-__device__ int4 find_rows(const TileParams &t, TileCtl &ctl, int m0, int r, bool reporter)
+// records: shared memory for the segments' copy, free until this returns.
+__device__ int4 find_rows(const TileParams &t, TileCtl &ctl, int4 *records, int capacity, int m0, int r, bool reporter)
 {
     const int lane = r & 31, warp = r >> 5;
     ctl.pos[r] = -1;
+    const SegmentTable segments = copy_segments(t, records, capacity, r, 128, reporter);
     named_sync(kRowBar, 128);
-    if (reporter) {
-        for (int g = r; g < t.n_segments; g += 128) {
-            int rank = 0;
-            float scale = 0.f;
-            const unsigned f = segment_problem(t, g, t.slots[g], t.offsets[g], t.offsets[g + 1], rank, scale);
-            if (f) atomicOr(t.status, f);
-        }
-    }
-    for (int q0 = 0; q0 < t.n_tokens; q0 += 512) {
-        int row[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int q = q0 + 128 * u + r;
-            row[u] = q < t.n_tokens && t.token_indices ? t.token_indices[q] : q;
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int q = q0 + 128 * u + r;
-            const int at = q < t.n_tokens ? claimed_row(t, q, row[u], m0, MR, reporter) : -1;
-            if (at >= 0 && atomicCAS(&ctl.pos[at], -1, q) != -1) atomicOr(t.status, kFlagBadRow);   // claimed twice
-        }
-    }
+    claim_rows(t, segments, m0, MR, ctl.pos, r, 128, reporter);
     named_sync(kRowBar, 128);
     int4 info = make_int4(-1, -1, 0, 0);
-    if (ctl.pos[r] >= 0) info = row_of_position(t, ctl.pos[r]);
+    if (ctl.pos[r] >= 0) info = row_of_position(t, segments, ctl.pos[r]);
     ctl.row_slot[r] = info.y;
     named_sync(kRowBar, 128);
     const bool first = first_with_slot(ctl.row_slot, r, info.y);
@@ -215,6 +196,7 @@ __global__ void __launch_bounds__(MT, 1)
 {
     using S = TileShape<RK>;
     constexpr int GS = S::GS, HOP = S::HOP;
+    static_assert(sizeof(TileCtl) <= 6144, "shared memory");
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ TileCtl ctl;
     uint8_t *ring = align_1024(smem_raw);
@@ -230,6 +212,8 @@ __global__ void __launch_bounds__(MT, 1)
         tmem_alloc(&ctl.tmem, T_COLS);
         tmem_relinquish();
     }
+    if (tid < 4) prefetch_map(tid == 0 ? &p.w_map : tid == 1 ? &p.x_map : tid == 2 ? &p.ws_map : &p.xs_map);
+    if (RK > 0 && tid >= 4 && tid < 8 && 8 << (tid - 4) <= RK) prefetch_map(&p.b_map[tid - 4]);
     if (tid == 0) {
         for (int s = 0; s < GS; ++s) {
             mbar_init(&ctl.full[s], 1);
@@ -249,11 +233,15 @@ __global__ void __launch_bounds__(MT, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    griddep_wait();   // from here on: what earlier kernels wrote
-    const uint32_t tmem = ctl.tmem;
     // this CTA's K blocks and adapter slots
     const int nkb = (p.d_in + KB - 1) / KB;
     const int kb0 = nkb * crank / ksplit, kb1 = nkb * (crank + 1) / ksplit;
+    // While earlier kernels finish: the weights' way into L2 (a copy of what they hold later is made
+    // only after the wait).
+    if (warp == 0 && mb == 0)
+        for (int kb = kb0 + lane; kb < kb1; kb += 32) tma_prefetch_2d(&p.w_map, kb * (KB / 2), n0);
+    griddep_wait();   // from here on: what earlier kernels wrote
+    const uint32_t tmem = ctl.tmem;
 
     if (warp == 0) {
         // (the whole warp walks the stages, one lane issues: see warp 1)
@@ -332,26 +320,30 @@ __global__ void __launch_bounds__(MT, 1)
             ok = __all_sync(0xffffffffu, mwait(p, ctl, &ctl.staged, 0));
             constexpr uint32_t idesc = umma_idesc_bf16(MR, MC);
             const int mine = (ctl.count - crank + ksplit - 1) / ksplit;
-            const uint32_t a_hi = smem_addr(hop), a_lo = a_hi + HOP;
+            const uint32_t a_hi = smem_addr(hop);
             for (int i0 = 0; i0 < mine && ok; i0 += S::SLOTS, ++g) {
                 const int s = (int)(g % GS), n = min(S::SLOTS, mine - i0);
                 ok = __all_sync(0xffffffffu, mwait(p, ctl, &ctl.full[s], (g / GS) & 1u));
                 if (!ok) break;
                 tc_fence_after();
+                const uint64_t ah = umma_desc_kmajor(a_hi, (MR / 8) * 128, 128), al = ah + (HOP >> 4);
+                const uint64_t b_s = umma_desc_kmajor(smem_addr(ring) + (uint32_t)s * STAGE, MC * 16, 128);
                 for (int i = 0; i < n; ++i) {
                     const int j = crank + (i0 + i) * ksplit, R = ctl.bucket[j];
                     const uint4 others = *reinterpret_cast<const uint4 *>(ctl.others[j]);
-                    const uint32_t b_s = smem_addr(ring) + (uint32_t)(s * STAGE + i * S::B_BYTES);
+                    uint64_t bd = b_s + (uint32_t)i * (S::B_BYTES >> 4);
+                    // bucket 8: the second rank group of B is the zero block
+                    if (R == 8) {
+                        const uint32_t b0 = smem_addr(ring) + (uint32_t)(s * STAGE + i * S::B_BYTES);
+                        bd = umma_desc_kmajor(b0, smem_addr(zero) - b0, 128);
+                    }
                     if (issuer) {
-                        for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
-                            const uint32_t b0 = b_s + st * 2 * MC * 16;
-                            // bucket 8: the second rank group of B is the zero block
-                            const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : MC * 16;
-                            const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
-                            const uint32_t koff = st * 2 * (MR / 8) * 128;
-                            umma_bf16_rows(tmem + T_LORA, umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd, idesc,
+#pragma unroll
+                        for (int st = 0; st < RK / 16; ++st) {
+                            if (16 * st >= R) break;
+                            umma_bf16_rows(tmem + T_LORA, ah + st * (2 * (MR / 8) * 128 >> 4), bd + st * (2 * MC), idesc,
                                            others);
-                            umma_bf16_rows(tmem + T_LORA, umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd, idesc,
+                            umma_bf16_rows(tmem + T_LORA, al + st * (2 * (MR / 8) * 128 >> 4), bd + st * (2 * MC), idesc,
                                            others);
                         }
                     }
@@ -367,7 +359,7 @@ __global__ void __launch_bounds__(MT, 1)
         const int r = tid - 64, quarter = warp & 3;
         bool lora = false;
         if constexpr (RK > 0) {
-            const int4 info = find_rows(sg.t, ctl, m0, r, blockIdx.x == 0);
+            const int4 info = find_rows(sg.t, ctl, reinterpret_cast<int4 *>(hop), 2 * HOP / 16, m0, r, blockIdx.x == 0);
             if (r == 0) mbar_arrive(&ctl.listed);
             lora = ctl.count > crank;   // this CTA has a slot
             if (lora) {
@@ -395,13 +387,11 @@ __global__ void __launch_bounds__(MT, 1)
             float *red = reinterpret_cast<float *>(ring) + (32 * quarter + lane) * RED_PITCH;
             const bool any = m0 + 32 * quarter < p.n_rows;   // a row of this warp exists
             for (int c = 0; c < MC && any; c += 32) {
-                uint32_t v[32];
+                uint32_t v[32], w[32];
                 tmem_ld32(tb + c, v);
+                if (lora) tmem_ld32(tb + T_LORA + c, w);
                 tmem_wait_ld();
                 if (lora) {
-                    uint32_t w[32];
-                    tmem_ld32(tb + T_LORA + c, w);
-                    tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
                 }
@@ -425,23 +415,33 @@ __global__ void __launch_bounds__(MT, 1)
     if (ksplit > 1) {
         cluster_arrive_release();
         cluster_wait_acquire();
-        // this CTA's share of the columns, summed over the cluster in CTA order
+        // this CTA's share of the columns, summed over the cluster in CTA order (all loads first)
         int bad = 0;
-        for (int c = 0; c < ksplit; ++c)
-            bad |= __float_as_int(ld_dsmem_f32(map_to_rank(smem_addr((const void *)&ctl.fail), (uint32_t)c)));
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            if (c < ksplit)
+                bad |= __float_as_int(ld_dsmem_f32(map_to_rank(smem_addr((const void *)&ctl.fail), (uint32_t)c)));
         const int rows = min(MR, p.n_rows - m0), share = MC / ksplit / 8;   // 8-column groups
-        for (int i = tid; i < rows * share && !bad; i += MT) {
+        for (int i = tid; i < rows * share; i += MT) {
             const int r = i / share, col = (crank * share + i % share) * 8;
             if (n0 + col >= p.d_out) continue;
             const uint32_t at = smem_addr(reinterpret_cast<float *>(ring) + r * RED_PITCH + col);
-            float f[8] = {};
-            for (int c = 0; c < ksplit; ++c) {
+            float4 a[8], b[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if (c >= ksplit) break;
                 const uint32_t src = map_to_rank(at, (uint32_t)c);
-                const float4 a = ld_dsmem_f32x4(src), b = ld_dsmem_f32x4(src + 16);
-                f[0] += a.x, f[1] += a.y, f[2] += a.z, f[3] += a.w;
-                f[4] += b.x, f[5] += b.y, f[6] += b.z, f[7] += b.w;
+                a[c] = ld_dsmem_f32x4(src);
+                b[c] = ld_dsmem_f32x4(src + 16);
             }
-            store8(p, m0 + r, n0 + col, f);
+            float f[8] = {};
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                if (c >= ksplit) break;
+                f[0] += a[c].x, f[1] += a[c].y, f[2] += a[c].z, f[3] += a[c].w;
+                f[4] += b[c].x, f[5] += b[c].y, f[6] += b[c].z, f[7] += b[c].w;
+            }
+            if (!bad) store8(p, m0 + r, n0 + col, f);
         }
         cluster_arrive_release();
         cluster_wait_acquire();
@@ -635,6 +635,7 @@ __global__ void __launch_bounds__(PT, 1)
         tmem_alloc_pair(&ctl.tmem, P_COLS);
         tmem_relinquish_pair();
     }
+    if (tid < 4) prefetch_map(tid == 0 ? &p.w_map : tid == 1 ? &p.x_map : tid == 2 ? &p.ws_map : &p.xs_map);
     if (tid == 0) {
         for (int s = 0; s < GS; ++s) {
             mbar_init(&ctl.full[s], 2);            // codes, scales
@@ -802,36 +803,39 @@ __global__ void __launch_bounds__(PT, 1)
                                                      pwait(p, ctl, &ctl.k_done, lc & 1u));
                     ++lc;
                     constexpr uint32_t idesc = umma_idesc_bf16(2 * MR, UN);
-                    const uint32_t a_hi = smem_addr(hop), a_lo = a_hi + HOP;
+                    const uint32_t a_hi = smem_addr(hop);
                     for (int i0 = 0; i0 < count && ok; i0 += SLOTS, ++g) {
                         const int s = (int)(g % GS), n = min(SLOTS, count - i0);
                         ok = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.full[s], (g / GS) & 1u));
                         if (!ok) break;
                         tc_fence_after();
+                        const uint64_t ah = umma_desc_kmajor(a_hi, (MR / 8) * 128, 128), al = ah + (HOP >> 4);
+                        const uint64_t b_s = umma_desc_kmajor(smem_addr(ring) + (uint32_t)s * S::STAGE, PH * 16, 128);
                         for (int i = 0; i < n; ++i) {
                             const int R = ctl.bucket[i0 + i];
                             const uint4 *others = reinterpret_cast<const uint4 *>(ctl.others[i0 + i]);
                             const uint4 o0 = others[0], o1 = others[1];
-                            const uint32_t b_i = smem_addr(ring) + (uint32_t)(s * S::STAGE + i * S::B_BYTES);
-                            if (issuer) {
 #pragma unroll
-                                for (int u = 0; u < NSUB; ++u) {
-                                    for (int st = 0; st < (R < 16 ? 16 : R) / 16; ++st) {
-                                        const uint32_t b0 = b_i + u * PH * RK * 2 + st * 2 * PH * 16;
-                                        // bucket 8: the second rank group of B is the zero block
-                                        const uint32_t lbo = R == 8 ? smem_addr(zero) - b0 : PH * 16;
-                                        const uint64_t bd = umma_desc_kmajor(b0, lbo, 128);
-                                        const uint32_t koff = st * 2 * (MR / 8) * 128;
-                                        umma_bf16_rows_pair(tmem + u * UN,
-                                                            umma_desc_kmajor(a_hi + koff, (MR / 8) * 128, 128), bd,
-                                                            idesc, o0, o1);
-                                        umma_bf16_rows_pair(tmem + u * UN,
-                                                            umma_desc_kmajor(a_lo + koff, (MR / 8) * 128, 128), bd,
-                                                            idesc, o0, o1);
+                            for (int u = 0; u < NSUB; ++u) {
+                                uint64_t bd = b_s + (uint32_t)i * (S::B_BYTES >> 4) + u * (PH * RK * 2 >> 4);
+                                // bucket 8: the second rank group of B is the zero block
+                                if (R == 8) {
+                                    const uint32_t b0 =
+                                        smem_addr(ring) + (uint32_t)(s * S::STAGE + i * S::B_BYTES + u * PH * RK * 2);
+                                    bd = umma_desc_kmajor(b0, smem_addr(zero) - b0, 128);
+                                }
+                                if (issuer) {
+#pragma unroll
+                                    for (int st = 0; st < RK / 16; ++st) {
+                                        if (16 * st >= R) break;
+                                        umma_bf16_rows_pair(tmem + u * UN, ah + st * (2 * (MR / 8) * 128 >> 4),
+                                                            bd + st * (2 * PH), idesc, o0, o1);
+                                        umma_bf16_rows_pair(tmem + u * UN, al + st * (2 * (MR / 8) * 128 >> 4),
+                                                            bd + st * (2 * PH), idesc, o0, o1);
                                     }
                                 }
+                                __syncwarp();
                             }
-                            __syncwarp();
                         }
                         if (issuer) umma_commit_pair(&ctl.empty[s], kPairMask);
                         __syncwarp();

@@ -125,32 +125,81 @@ __device__ __forceinline__ int segment_of_position(const TileParams &p, int q)
     return lo;
 }
 
-// Grouped position q's claim on a row of [row0, row0 + n): the position's row if its segment is a
-// valid adapter segment.  `reporter` flags rows that do not exist; returns the row's index in the
-// block, or -1.
-__device__ __forceinline__ int claimed_row(const TileParams &p, int q, int row, int row0, int n, bool reporter)
+// A block's copy of the segments in shared memory, {first position, slot (-1: base or invalid), scale,
+// rank} each: a search through L2 is a chain of dependent loads of 0.4 us each (256 rows of 64
+// slots took 5 us to find so).  An end record closes it.
+struct SegmentTable {
+    int4 *records;   // null: too many segments, they are read where they are
+    int n;
+};
+
+// All `threads` of the caller take part; it synchronises them afterwards.  `reporter` flags the
+// segments' problems.
+__device__ __forceinline__ SegmentTable copy_segments(const TileParams &p, int4 *records, int capacity, int tid,
+                                                      int threads, bool reporter)
 {
-    const bool exists = row >= 0 && row < p.n_rows;
-    const bool in = exists && row >= row0 && row < row0 + n;
-    if (!in && !(reporter && !exists)) return -1;
+    SegmentTable t{p.n_segments < capacity ? records : nullptr, p.n_segments};
+    if (t.records == nullptr && !reporter) return t;
+    for (int g = tid; g < p.n_segments; g += threads) {
+        const int p0 = p.offsets[g], p1 = p.offsets[g + 1], a = p.slots[g];
+        int rank = 0;
+        float scale = 0.f;
+        const unsigned f = segment_problem(p, g, a, p0, p1, rank, scale);
+        if (f && reporter) atomicOr(p.status, f);
+        // (an end that differs from the next segment's beginning is no valid segment's)
+        if (t.records) records[g] = make_int4(p0, f || a < 0 ? -1 : a, __float_as_int(scale), rank);
+    }
+    if (t.records && tid == 0) records[p.n_segments] = make_int4(p.offsets[p.n_segments], -1, 0, 0);
+    return t;
+}
+
+// {q, slot, scale, rank} of grouped position q if it lies in a valid adapter segment, else {-1, ...}.
+__device__ __forceinline__ int4 row_of_position(const TileParams &p, const SegmentTable &t, int q)
+{
+    const int4 none = make_int4(-1, -1, 0, 0);
+    if (t.records) {
+        int lo = 0, hi = t.n - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (t.records[mid].x <= q) lo = mid;
+            else hi = mid - 1;
+        }
+        const int4 v = t.records[lo];
+        if (v.y < 0 || q < v.x || q >= t.records[lo + 1].x) return none;
+        return make_int4(q, v.y, v.z, v.w);
+    }
     const int g = segment_of_position(p, q);
     const int a = p.slots[g], p0 = p.offsets[g], p1 = p.offsets[g + 1];
     int rank = 0;
     float scale = 0.f;
-    if (a < 0 || q < p0 || q >= p1 || segment_problem(p, g, a, p0, p1, rank, scale)) return -1;
-    if (in) return row - row0;
-    atomicOr(p.status, kFlagBadRow);
-    return -1;
+    if (a < 0 || q < p0 || q >= p1 || segment_problem(p, g, a, p0, p1, rank, scale)) return none;
+    return make_int4(q, a, __float_as_int(scale), rank);
 }
 
-// {position, slot, scale, rank} of a claimed position.
-__device__ __forceinline__ int4 row_of_position(const TileParams &p, int q)
+// Finds the rows of a block [row0, row0 + n): claims[r] (preset to -1) gets the grouped position that
+// names row r and lies in a valid adapter segment.  A row claimed twice keeps one claim and is flagged;
+// `reporter` flags rows that do not exist.
+__device__ __forceinline__ void claim_rows(const TileParams &p, const SegmentTable &t, int row0, int n, int *claims,
+                                           int tid, int threads, bool reporter)
 {
-    const int g = segment_of_position(p, q), a = p.slots[g];
-    int rank = 0;
-    float scale = 0.f;
-    segment_problem(p, g, a, p.offsets[g], p.offsets[g + 1], rank, scale);
-    return make_int4(q, a, __float_as_int(scale), rank);
+    for (int64_t q0 = tid; q0 < p.n_tokens; q0 += 4 * threads) {
+        int row[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t q = q0 + u * threads;
+            row[u] = q < p.n_tokens && p.token_indices ? p.token_indices[q] : (int)q;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t q = q0 + u * threads;
+            if (q >= p.n_tokens) continue;
+            const bool exists = row[u] >= 0 && row[u] < p.n_rows;
+            const bool in = exists && row[u] >= row0 && row[u] < row0 + n;
+            if (!in && !(reporter && !exists)) continue;
+            if (row_of_position(p, t, (int)q).x < 0) continue;
+            if (!in || atomicCAS(&claims[row[u] - row0], -1, (int)q) != -1) atomicOr(p.status, kFlagBadRow);
+        }
+    }
 }
 
 // Whether row r is the first of its block with this slot (>= 0); slots[] in shared memory,
