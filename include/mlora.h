@@ -204,7 +204,8 @@ mlora_status mlora_expand(mlora_pool *pool, const mlora_segments *segs, const fl
  * rows it passes through an fp32 workspace the pool owns (grown, stream-ordered on
  * `stream` with no device-wide synchronisation, when a batch needs more; growth is
  * not possible during stream capture: MLORA_ERR_UNSUPPORTED, so run the largest
- * batch once before capturing).  Calls on one pool whose kernels overlap on the GPU
+ * batch once before capturing; outgrown buffers are kept until the pool is destroyed, so
+ * that graphs captured before stay valid).  Calls on one pool whose kernels overlap on the GPU
  * (several streams) share that workspace and race on it: serialise them, give each
  * stream its own pool, or use mlora_shrink / mlora_expand with caller-owned H.
  * X: device bf16 [n_rows, d_in]; Y: device bf16 [n_rows, d_out].
@@ -432,7 +433,7 @@ mlora_status mlora_build_segments(const int32_t *row_slots, int32_t n_rows,
  * first, where the segments' rows are consecutive (token_indices NULL, n_rows = N).
  * An entry that is no slot of the pool (< -1 or >= n_slots) is in no segment: its position
  * is -1, order lists it behind offsets[S], and MLORA_FLAG_BAD_SLOT is set.
- * MLORA_ERR_UNSUPPORTED for a pool of more than 12798 slots.
+ * N is at most 2^30.  MLORA_ERR_UNSUPPORTED for a pool of more than 12798 slots.
  */
 typedef struct {
     int32_t *offsets;

@@ -381,17 +381,22 @@ def _float_code(t, what: str) -> int:
     return code
 
 
+_current_device = _raw_stream = None   # torch's, looked up once: a small call is mostly such look-ups
+
+
 def _call(fn, what: str, device: int, stream, *args) -> None:
     """fn(*args, stream) with `device` current, on its current stream unless one is given."""
-    import torch
+    global _current_device, _raw_stream
+    if _current_device is None:
+        import torch
+        _current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
     if device < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    if device != torch.cuda.current_device():
+    if device != _current_device():
+        import torch
         with torch.cuda.device(device):
             return _call(fn, what, device, stream, *args)
-    # (the raw handle: making a Stream object costs more than the call)
-    s = torch._C._cuda_getCurrentRawStream(device) if stream is None else _stream_ptr(stream)
-    st = fn(*args, s)
+    st = fn(*args, _raw_stream(device) if stream is None else _stream_ptr(stream))
     if st != OK:
         raise MloraError(st, what)
 
@@ -521,9 +526,11 @@ class RowGroups:
     """Rows grouped by slot on the device (mlora_group_rows), usable as DeviceSegments: of the
     batch's own rows with one slot per row, of the rows in grouped order (gather_rows) with more.
 
-    offsets, slots, ranks, order, positions: int32 device tensors (see mlora.h)."""
+    offsets, slots, ranks, order, positions: int32 device tensors (see mlora.h).  ranks are this pool's;
+    with_ranks=False leaves them out of the segments, for use with pools whose ranks differ."""
 
-    def __init__(self, pool: Pool, n_rows: int, top_k: int, device, max_segment_rows: int = 0, stream=None):
+    def __init__(self, pool: Pool, n_rows: int, top_k: int, device, max_segment_rows: int = 0, stream=None,
+                 with_ranks: bool = True):
         import torch
         n = n_rows * top_k
         S = min(pool.n_slots + 1, n)
@@ -535,11 +542,11 @@ class RowGroups:
         offsets, slots, ranks, order, self._positions = at, at + 4 * (S + 1), at + 4 * (2 * S + 1), at + 4 * (
             3 * S + 1), at + 4 * (3 * S + 1 + n)
         self._out = RowGroupsStruct(offsets, slots, ranks, order, self._positions)
-        self.struct = SegmentsStruct(S, n, n, int(max_segment_rows), offsets, slots, ranks, None,
+        self.struct = SegmentsStruct(S, n, n, int(max_segment_rows), offsets, slots, ranks if with_ranks else None, None,
                                      order if top_k == 1 else None, None)
 
     def _part(self, first: int, count: int):
-        return self._buf[first:first + count]
+        return self._buf.narrow(0, first, count)
 
     @property
     def offsets(self):
@@ -563,10 +570,11 @@ class RowGroups:
 
 
 def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segment_rows: int = 0,
-               stream=None) -> RowGroups:
+               stream=None, with_ranks: bool = True) -> RowGroups:
     """Sort rows by adapter slot on the device (mlora_group_rows).  row_slots: int32 [n_rows] or
     [n_rows, top_k], contiguous, -1 = base model.  `out` reuses a RowGroups of the same sizes (a
-    captured graph's).  max_segment_rows: the hint of mlora_segments, if the caller knows one."""
+    captured graph's).  max_segment_rows: the hint of mlora_segments, if the caller knows one;
+    with_ranks: see RowGroups (both only without `out`)."""
     import torch
     shape = row_slots.shape
     if row_slots.dtype != torch.int32 or len(shape) not in (1, 2) or not row_slots.is_contiguous():
@@ -575,7 +583,7 @@ def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segme
     if top_k < 1 or index < 0:
         raise ValueError("row_slots needs at least one slot per row, on a CUDA device")
     if out is None:
-        out = RowGroups(pool, n_rows, top_k, row_slots.device, max_segment_rows, stream)
+        out = RowGroups(pool, n_rows, top_k, row_slots.device, max_segment_rows, stream, with_ranks)
     elif out.pool is not pool or (out.n_rows, out.top_k, out._index) != (n_rows, top_k, index):
         raise ValueError("out must be of this pool, the same sizes and device")
     _call(lib().mlora_group_rows, "mlora_group_rows", index, stream, pool.handle, row_slots.data_ptr(), n_rows, top_k,

@@ -38,6 +38,7 @@ struct mlora_pool {
     std::vector<uint32_t> h_gen;
     float *ws;              // H partial sums of the long-segment kernels (grown on demand)
     size_t ws_bytes;
+    std::vector<float *> ws_old;   // outgrown ones
     std::mutex ws_mutex;
     // TMA views of the B blocks for rank buckets 8, 16, 32, 64 (those <= r_bucket_max):
     // one load brings one 128-column chunk of one slot's B, all its rank groups
@@ -223,27 +224,25 @@ bool encode_b_map_wide(CUtensorMap *map, const mlora_pool *pool, int R, int cols
 
 // Make the pool's workspace hold `bytes` (the caller holds pool->ws_mutex and keeps it
 // until the kernels that use the workspace are launched, so that no other thread frees
-// it in between).  Growth is stream-ordered (the old buffer is freed, and the new one
-// allocated, on `stream`: no device-wide synchronisation); it is not possible while
-// the stream is being captured.
+// it in between).  Growth is stream-ordered (no device-wide synchronisation); it is not
+// possible while the stream is being captured.
 mlora_status ensure_workspace(mlora_pool *pool, size_t bytes, cudaStream_t stream)
 {
     if (pool->ws_bytes >= bytes) return MLORA_OK;
     cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
     if (cudaStreamIsCapturing(stream, &cs) != cudaSuccess) return MLORA_ERR_CUDA;
     if (cs != cudaStreamCaptureStatusNone) return MLORA_ERR_UNSUPPORTED;
-    if (pool->ws) {
-        if (cudaFreeAsync(pool->ws, stream) != cudaSuccess) return MLORA_ERR_CUDA;
-        pool->ws = nullptr;
-        pool->ws_bytes = 0;
-    }
-    // some headroom, so that a slowly growing batch does not reallocate every call
-    const size_t want = std::max<size_t>(bytes + bytes / 4, (size_t)1 << 20);
-    if (cudaMallocAsync(reinterpret_cast<void **>(&pool->ws), want, stream) != cudaSuccess) {
+    // some headroom, so that a slowly growing batch does not reallocate every call; and at least
+    // twice the last buffer, so that those kept never add up to more than the current one
+    const size_t want = std::max({bytes + bytes / 4, 2 * pool->ws_bytes, (size_t)1 << 20});
+    float *fresh = nullptr;
+    if (cudaMallocAsync(reinterpret_cast<void **>(&fresh), want, stream) != cudaSuccess) {
         cudaGetLastError();
-        pool->ws = nullptr;
         return MLORA_ERR_OUT_OF_MEMORY;
     }
+    // The old buffer is kept: a captured graph may hold its address.
+    if (pool->ws) pool->ws_old.push_back(pool->ws);
+    pool->ws = fresh;
     pool->ws_bytes = want;
     return MLORA_OK;
 }
@@ -505,8 +504,9 @@ mlora_status mlora_pool_destroy(mlora_pool *pool)
     if (pool->d_scale) cudaFree(pool->d_scale);
     if (pool->d_gen) cudaFree(pool->d_gen);
     if (pool->d_status) cudaFree(pool->d_status);
-    if (pool->ws) {   // stream-ordered allocation: freed the same way, then waited for
+    if (pool->ws) {   // stream-ordered allocations: freed the same way, then waited for
         cudaFreeAsync(pool->ws, nullptr);
+        for (float *old : pool->ws_old) cudaFreeAsync(old, nullptr);
         cudaDeviceSynchronize();
     }
     delete pool;

@@ -112,7 +112,7 @@ struct MxRows {
 // Warp -> (128-row tile, r of 0..31, 256-column chunk).
 __device__ __forceinline__ bool my_unit(const MxRows &q, int64_t w, int &row0, int &chunk)
 {
-    const int64_t tiles = (q.n_rows + kTileRowsMx - 1) / kTileRowsMx;
+    const int64_t tiles = ((int64_t)q.n_rows + kTileRowsMx - 1) / kTileRowsMx;
     if (w >= tiles * 32 * q.chunks) return false;
     chunk = (int)(w % q.chunks);
     const int64_t r = w / q.chunks;

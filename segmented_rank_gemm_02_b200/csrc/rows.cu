@@ -40,6 +40,7 @@ constexpr int kGroupMaxWarps = 32;
 constexpr int kGroupMaxCluster = 8;
 constexpr int kGroupSmem = 200 * 1024;
 constexpr int kGroupTables = 4;   // besides the warps' tables: CTA totals, totals, first position, spare
+constexpr int64_t kMaxEntries = (int64_t)1 << 30;   // 32-bit positions, with room for a block's stride
 
 struct GroupParams {
     const int32_t *row_slots;
@@ -512,7 +513,7 @@ mlora_status row_common(mlora_pool *pool, const int32_t *positions, int32_t n_ro
     if (!mlora_pool_get_view(pool, &view)) return MLORA_ERR_INVALID_ARG;
     const int size = dtype_size(dtype);
     if (n_rows < 0 || top_k < 1 || n_tokens < 0 || d < 1 || size == 0) return MLORA_ERR_INVALID_ARG;
-    if ((int64_t)n_rows * top_k > INT32_MAX) return MLORA_ERR_INVALID_ARG;
+    if ((int64_t)n_rows * top_k > kMaxEntries) return MLORA_ERR_INVALID_ARG;
     if (((int64_t)d * size) % 16 != 0) return MLORA_ERR_UNSUPPORTED;   // rows of whole 16-byte vectors
     if (n_rows > 0 && positions == nullptr) return MLORA_ERR_INVALID_ARG;
     p.positions = positions;
@@ -552,7 +553,7 @@ mlora_status mlora_group_rows(mlora_pool *pool, const int32_t *row_slots, int32_
     mlora_pool_view view;
     if (!mlora_pool_get_view(pool, &view) || out == nullptr || n_rows < 0 || top_k < 1) return MLORA_ERR_INVALID_ARG;
     const int64_t n = (int64_t)n_rows * top_k;
-    if (n > INT32_MAX) return MLORA_ERR_INVALID_ARG;
+    if (n > kMaxEntries) return MLORA_ERR_INVALID_ARG;
     if (out->offsets == nullptr) return MLORA_ERR_INVALID_ARG;
     if (n > 0 && (row_slots == nullptr || out->slots == nullptr || out->order == nullptr || out->positions == nullptr))
         return MLORA_ERR_INVALID_ARG;

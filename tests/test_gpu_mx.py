@@ -315,3 +315,78 @@ def test_matches_the_oracle_entry():
     assert flags == 0
     err = np.abs(Y.cpu().double().numpy() - ref)
     assert (err <= 1e-2 * (1 + np.abs(ref))).all()
+
+
+def test_graph_outlives_a_grown_workspace():
+    # a graph captured while the pool's workspace was small still runs after a larger batch grew it
+    n, d_in, d_out = 40, 64, 64
+    pool, slot, slot_rank, A, B, X, W = _case(n, d_in, d_out, 3, (64,), 0.0, False, 81)
+    segs = mlora.DeviceSegments(mlora.build_segments(slot, pool), n, DEVICE)
+    Xd = X.to(DEVICE)
+    Xq, Wq = mlora.mx_quantize(Xd), mlora.mx_quantize(W.to(DEVICE))
+    Y = torch.zeros(n, d_out, dtype=torch.float32, device=DEVICE)
+    mlora.mx_gemm_apply(pool, segs, Xd, Xq, Wq, Y)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        mlora.mx_gemm_apply(pool, segs, Xd, Xq, Wq, Y)
+    big = 9000                      # 9000 x 64 fp32 of H: more than the first MiB
+    slot2 = np.resize(slot, big).astype(np.int32)
+    X2 = _rows(big, d_in, torch.bfloat16, 5, spread=1.0)
+    segs2 = mlora.DeviceSegments(mlora.build_segments(slot2, pool), big, DEVICE)
+    X2d = X2.to(DEVICE)
+    Y2 = torch.full((big, d_out), float("nan"), dtype=torch.float32, device=DEVICE)
+    mlora.mx_gemm_apply(pool, segs2, X2d, mlora.mx_quantize(X2d), Wq, Y2)
+    filler = [torch.full((1 << 18,), float("nan"), device=DEVICE) for _ in range(8)]
+    Y.fill_(float("nan"))
+    g.replay()
+    torch.cuda.synchronize()
+    _assert_product(Y, *_reference(slot, slot_rank, A, B, X, W), d_in)
+    rows = np.arange(0, big, 111)
+    _assert_product(Y2[torch.from_numpy(rows).to(DEVICE)], *_reference(slot2, slot_rank, A, B, X2, W, rows), d_in)
+    assert pool.check() == 0
+    del filler
+
+
+@pytest.mark.parametrize("n_rows", [200, 34000])
+def test_row_lookup_of_many_segments_and_rows(n_rows):
+    """More segments than a block keeps in shared memory, and more rows than the one-launch lookup
+    takes: every row its own segment (200 rows; the adapters' slots repeat), or runs of 16."""
+    d, n_slots = 64, 7
+    run = 1 if n_rows <= 1024 else 16
+    pool, _, slot_rank, A, B, X, W = _case(n_rows, d, d, n_slots, (8, 16), 0.0, False, 91)
+    seg_slot = np.random.default_rng(5).integers(-1, n_slots, n_rows // run).astype(np.int32)
+    # 200 rows: pad with empty segments, so that the list is longer than any table in shared memory
+    pad = 3000 if n_rows <= 1024 else 0
+    offsets = np.concatenate([np.arange(0, n_rows + 1, run), np.full(pad, n_rows)]).astype(np.int32)
+    perm = np.random.default_rng(6).permutation(n_rows).astype(np.int32)
+    meta = {"offsets": offsets, "slots": np.concatenate([seg_slot, np.full(pad, -1)]).astype(np.int32),
+            "token_indices": perm, "max_segment_rows": run}
+    slot = np.empty(n_rows, np.int32)
+    slot[perm] = seg_slot.repeat(run)
+    segs = mlora.DeviceSegments(meta, n_rows, DEVICE)
+    Xd = X.to(DEVICE)
+    Y = torch.full((n_rows, d), float("nan"), dtype=torch.float32, device=DEVICE)
+    mlora.mx_gemm_apply(pool, segs, Xd, mlora.mx_quantize(Xd), mlora.mx_quantize(W.to(DEVICE)), Y)
+    assert pool.check() == 0 and not torch.isnan(Y).any()
+    rows = np.arange(0, n_rows, max(1, n_rows // 300))
+    _assert_product(Y[torch.from_numpy(rows).to(DEVICE)], *_reference(slot, slot_rank, A, B, X, W, rows), d)
+    free()
+
+
+def test_rows_claimed_twice_or_missing_are_flagged():
+    n, d = 96, 64
+    pool, _, slot_rank, A, B, X, W = _case(n, d, d, 2, (16,), 0.0, False, 95)
+    ti = np.arange(n, dtype=np.int32)
+    ti[50] = 3                       # row 3 named twice, row 50 not at all
+    ti[60] = n + 5                   # no such row
+    meta = {"offsets": np.array([0, 40, n], np.int32), "slots": np.array([0, 1], np.int32), "token_indices": ti,
+            "max_segment_rows": 1}
+    segs = mlora.DeviceSegments(meta, n, DEVICE)
+    Xd = X.to(DEVICE)
+    Y = torch.full((n, d), float("nan"), dtype=torch.float32, device=DEVICE)
+    mlora.mx_gemm_apply(pool, segs, Xd, mlora.mx_quantize(Xd), mlora.mx_quantize(W.to(DEVICE)), Y)
+    assert pool.check() & mlora.FLAG_BAD_ROW
+    slot = np.where(np.arange(n) < 40, 0, 1)
+    slot[[50, 60]] = -1
+    rows = np.array([t for t in range(n) if t != 3])
+    _assert_product(Y[torch.from_numpy(rows).to(DEVICE)], *_reference(slot, slot_rank, A, B, X, W, rows), d)
