@@ -524,7 +524,8 @@ def mx_gemm_apply(pool: Pool, segs: Optional["DeviceSegments"], X, Xq: MxMatrix,
 
 class RowGroups:
     """Rows grouped by slot on the device (mlora_group_rows), usable as DeviceSegments: of the
-    batch's own rows with one slot per row, of the rows in grouped order (gather_rows) with more.
+    batch's own rows with one slot per row, of the rows in grouped order (gather_rows) with more
+    (grouped() gives the latter in either case).
 
     offsets, slots, ranks, order, positions: int32 device tensors (see mlora.h).  ranks are this pool's;
     with_ranks=False leaves them out of the segments, for use with pools whose ranks differ."""
@@ -544,6 +545,10 @@ class RowGroups:
         self._out = RowGroupsStruct(offsets, slots, ranks, order, self._positions)
         self.struct = SegmentsStruct(S, n, n, int(max_segment_rows), offsets, slots, ranks if with_ranks else None, None,
                                      order if top_k == 1 else None, None)
+
+    def grouped(self) -> "_GroupedSegments":
+        """The segments of the rows in grouped order (those of gather_rows), whatever top_k is."""
+        return _GroupedSegments(self)
 
     def _part(self, first: int, count: int):
         return self._buf.narrow(0, first, count)
@@ -567,6 +572,14 @@ class RowGroups:
     @property
     def positions(self):
         return self._part(3 * self._S + 1 + self.n_tokens, self.n_tokens)
+
+
+class _GroupedSegments:
+    def __init__(self, groups: RowGroups):
+        s = groups.struct
+        self.groups, self.n_tokens = groups, groups.n_tokens   # (keeps the arrays)
+        self.struct = SegmentsStruct(s.n_segments, s.n_rows, s.n_tokens, s.max_segment_rows, s.segment_offsets,
+                                     s.adapter_slots, s.ranks, None, None, None)
 
 
 def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segment_rows: int = 0,

@@ -95,6 +95,20 @@ def test_group_ranks_and_apply():
     assert ((Y1.double() - Y2.double()).abs() <= 2.0 ** -7 * (Y2.double().abs() + 2.0 ** -6)).all()
     base = torch.from_numpy(slots[:, 0] < 0).to(DEVICE)
     assert torch.equal(Y1[base], Y0[base])
+    # the rows in grouped order, where a slot's rows stand together, and back
+    Ys = mlora.gather_rows(gr, Y0)
+    mlora.apply(pool, gr.grouped(), mlora.gather_rows(gr, X), Ys)
+    Y3 = mlora.combine_rows(gr, Ys)
+    assert pool.check() == 0
+    assert ((Y3.double() - Y2.double()).abs() <= 2.0 ** -7 * (Y2.double().abs() + 2.0 ** -6)).all()
+    # ranks of another pool may differ: its segments go without them
+    other = mlora.Pool(d, 64, 9, 8)
+    for a in range(9):
+        other.load_slot(a, 4, 4.0, torch.zeros(4, d, dtype=torch.bfloat16, device=DEVICE),
+                        torch.zeros(64, 4, dtype=torch.bfloat16, device=DEVICE))
+    Z = torch.ones(n, 64, dtype=torch.bfloat16, device=DEVICE)
+    mlora.apply(other, mlora.group_rows(pool, torch.from_numpy(slots[:, 0].copy()).to(DEVICE), with_ranks=False), X, Z)
+    assert other.check() == 0 and (Z == 1).all()
 
 
 ROWS = [(1, 1, 8), (1, 2, 4096), (5, 3, 40), (64, 1, 512), (33, 2, 1032), (257, 4, 2048), (100, 8, 256), (40, 5, 8192),
