@@ -401,15 +401,16 @@ def _call(fn, what: str, device: int, stream, *args) -> None:
         raise MloraError(st, what)
 
 
-def _empty(shape, dtype, device, stream):
-    """An output for a call on `stream`: allocated there, so that its memory is not still in use elsewhere."""
-    import torch
+def _empty(like, shape, dtype, stream):
+    """An output on like's device for a call on `stream`: allocated there, so that its memory is not
+    still in use elsewhere."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape) if dtype is None else like.new_empty(shape, dtype=dtype)
+    import torch
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype or like.dtype)
 
 
 class MxMatrix:
@@ -417,7 +418,7 @@ class MxMatrix:
     columns] and scale tiles [ceil(n_rows / 128), 2 ceil(n_cols / 256), 32, 4, 4], uint8, allocated
     on `device` or given (a checkpoint's own, already in this layout)."""
 
-    def __init__(self, n_rows: int, n_cols: int, device=None, codes=None, scales=None, stream=None):
+    def __init__(self, n_rows: int, n_cols: int, device=None, codes=None, scales=None, stream=None, like=None):
         import torch
         n_rows, n_cols = int(n_rows), int(n_cols)
         if n_rows < 0 or n_cols <= 0 or n_cols % 8 != 0:
@@ -428,7 +429,9 @@ class MxMatrix:
         if codes is None and scales is None:
             # one allocation: the scale tiles (whole 1 KB), then the codes; the tensors are made when asked for
             at = (n_rows + 127) // 128 * ((n_cols + 255) // 256) * 1024
-            self._buf = _empty(at + n_rows * row_bytes, torch.uint8, device, stream)
+            if like is None:
+                like = torch.empty(0, dtype=torch.uint8, device=device)
+            self._buf = _empty(like, at + n_rows * row_bytes, torch.uint8, stream)
             ptr = self._buf.data_ptr()
             self._index = self._buf.get_device()
             self.struct = MxStruct(n_rows, n_cols, row_bytes, ptr + at, ptr)
@@ -477,7 +480,7 @@ def mx_quantize(X, out: Optional[MxMatrix] = None, stream=None) -> MxMatrix:
     if index < 0:
         raise ValueError("X must be on a CUDA device")
     if out is None:
-        out = MxMatrix(n, d, X.device, stream=stream)
+        out = MxMatrix(n, d, stream=stream, like=X)
     elif (out.n_rows, out.n_cols, out._index) != (n, d, index):
         raise ValueError("out must have X's shape and device")
     _call(lib().mlora_mx_quantize, "mlora_mx_quantize", index, stream, X.data_ptr(), code,
@@ -490,7 +493,7 @@ def mx_dequantize(Q: MxMatrix, out=None, dtype=None, stream=None):
     import torch
     shape = (Q.n_rows, Q.n_cols)
     if out is None:
-        out = _empty(shape, dtype or torch.bfloat16, Q.device, stream)
+        out = _empty(Q._buf if Q._codes is None else Q._codes, shape, dtype or torch.bfloat16, stream)
     elif tuple(out.shape) != shape or out.get_device() != Q._index or dtype not in (None, out.dtype):
         raise ValueError("out must have Q's shape and device, and dtype if both are given")
     ld = _ld(out, "out")
@@ -530,21 +533,32 @@ class RowGroups:
     offsets, slots, ranks, order, positions: int32 device tensors (see mlora.h).  ranks are this pool's;
     with_ranks=False leaves them out of the segments, for use with pools whose ranks differ."""
 
-    def __init__(self, pool: Pool, n_rows: int, top_k: int, device, max_segment_rows: int = 0, stream=None,
-                 with_ranks: bool = True):
+    def __init__(self, pool: Pool, n_rows: int, top_k: int, device=None, max_segment_rows: int = 0, stream=None,
+                 with_ranks: bool = True, like=None):
         import torch
         n = n_rows * top_k
         S = min(pool.n_slots + 1, n)
         self.pool, self.n_rows, self.top_k, self.n_tokens, self._S = pool, n_rows, top_k, n, S
         # one allocation; the tensors are made when asked for
-        self._buf = _empty(3 * S + 1 + 2 * n, torch.int32, device, stream)
+        if like is None:
+            like = torch.empty(0, dtype=torch.int32, device=device)
+        self._buf = _empty(like, 3 * S + 1 + 2 * n, torch.int32, stream)
         self._index = self._buf.get_device()
         at = self._buf.data_ptr()
-        offsets, slots, ranks, order, self._positions = at, at + 4 * (S + 1), at + 4 * (2 * S + 1), at + 4 * (
-            3 * S + 1), at + 4 * (3 * S + 1 + n)
-        self._out = RowGroupsStruct(offsets, slots, ranks, order, self._positions)
-        self.struct = SegmentsStruct(S, n, n, int(max_segment_rows), offsets, slots, ranks if with_ranks else None, None,
-                                     order if top_k == 1 else None, None)
+        self._positions = at + 4 * (3 * S + 1 + n)
+        self._out = RowGroupsStruct(at, at + 4 * (S + 1), at + 4 * (2 * S + 1), at + 4 * (3 * S + 1), self._positions)
+        self._hint, self._with_ranks, self._struct = int(max_segment_rows), with_ranks, None
+
+    def _segments(self, own_rows: bool) -> SegmentsStruct:
+        o, n = self._out, self.n_tokens
+        return SegmentsStruct(self._S, n, n, self._hint, o.offsets, o.slots, o.ranks if self._with_ranks else None, None,
+                              o.order if own_rows else None, None)
+
+    @property
+    def struct(self) -> SegmentsStruct:
+        if self._struct is None:
+            self._struct = self._segments(self.top_k == 1)
+        return self._struct
 
     def grouped(self) -> "_GroupedSegments":
         """The segments of the rows in grouped order (those of gather_rows), whatever top_k is."""
@@ -576,10 +590,8 @@ class RowGroups:
 
 class _GroupedSegments:
     def __init__(self, groups: RowGroups):
-        s = groups.struct
         self.groups, self.n_tokens = groups, groups.n_tokens   # (keeps the arrays)
-        self.struct = SegmentsStruct(s.n_segments, s.n_rows, s.n_tokens, s.max_segment_rows, s.segment_offsets,
-                                     s.adapter_slots, s.ranks, None, None, None)
+        self.struct = groups._segments(False)
 
 
 def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segment_rows: int = 0,
@@ -596,7 +608,7 @@ def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segme
     if top_k < 1 or index < 0:
         raise ValueError("row_slots needs at least one slot per row, on a CUDA device")
     if out is None:
-        out = RowGroups(pool, n_rows, top_k, row_slots.device, max_segment_rows, stream, with_ranks)
+        out = RowGroups(pool, n_rows, top_k, None, max_segment_rows, stream, with_ranks, row_slots)
     elif out.pool is not pool or (out.n_rows, out.top_k, out._index) != (n_rows, top_k, index):
         raise ValueError("out must be of this pool, the same sizes and device")
     _call(lib().mlora_group_rows, "mlora_group_rows", index, stream, pool.handle, row_slots.data_ptr(), n_rows, top_k,
@@ -628,7 +640,7 @@ def gather_rows(groups: RowGroups, X, Xs=None, stream=None):
     code, d, n, index = _float_code(X, "X"), X.shape[-1], groups.n_tokens, groups._index
     ldx = _rows_of(X, groups.n_rows, d, X.dtype, index, "X")
     if Xs is None:
-        Xs, ldxs = _empty((n, d), X.dtype, X.device, stream), d
+        Xs, ldxs = _empty(X, (n, d), None, stream), d
     else:
         ldxs = _rows_of(Xs, n, d, X.dtype, index, "Xs")
     _call(lib().mlora_gather_rows, "mlora_gather_rows", index, stream, groups.pool.handle, groups._positions,
@@ -642,7 +654,7 @@ def combine_rows(groups: RowGroups, Ys, weights=None, Y=None, stream=None):
     ldys = _rows_of(Ys, n, d, Ys.dtype, index, "Ys")
     w = _weights_ptr(groups, weights, index, "weights")
     if Y is None:
-        Y, ldy = _empty((groups.n_rows, d), Ys.dtype, Ys.device, stream), d
+        Y, ldy = _empty(Ys, (groups.n_rows, d), None, stream), d
     else:
         ldy = _rows_of(Y, groups.n_rows, d, Ys.dtype, index, "Y")
     _call(lib().mlora_combine_rows, "mlora_combine_rows", index, stream, groups.pool.handle, groups._positions, w,
@@ -658,11 +670,11 @@ def combine_rows_backward(groups: RowGroups, dY, Ys, weights=None, dYs=None, dwe
     lddy = _rows_of(dY, groups.n_rows, d, dY.dtype, index, "dY")
     w = _weights_ptr(groups, weights, index, "weights")
     if dYs is None:
-        dYs, lddys = _empty((n, d), dY.dtype, dY.device, stream), d
+        dYs, lddys = _empty(dY, (n, d), None, stream), d
     else:
         lddys = _rows_of(dYs, n, d, dY.dtype, index, "dYs")
     if dweights is None and weights is not None:
-        dweights = _empty((groups.n_rows, groups.top_k), torch.float32, dY.device, stream)
+        dweights = _empty(dY, (groups.n_rows, groups.top_k), torch.float32, stream)
     dw = _weights_ptr(groups, dweights, index, "dweights")
     if dw is not None and Ys is None:
         raise ValueError("the gradient of the weights needs Ys")

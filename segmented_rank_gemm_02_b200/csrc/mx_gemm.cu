@@ -576,26 +576,20 @@ __device__ __forceinline__ void transpose8(uint4 (&a)[8], int k)
     }
 }
 
-// 64 columns of this lane's row out of tensor memory, rounded to 16 bits: eight 16-byte pieces.
+// 64 fp32 columns of this lane's row, rounded to 16 bits: eight 16-byte pieces.
 template <int YT>
-__device__ __forceinline__ void take64(uint32_t taddr, uint4 (&a)[8])
+__device__ __forceinline__ void round64(const uint32_t (&v)[2][32], uint4 (&a)[8])
 {
-    uint32_t v2[2][32];
-    tmem_ld32(taddr, v2[0]);
-    tmem_ld32(taddr + 32, v2[1]);
-    tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-        const uint32_t (&v)[32] = v2[c];
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                w[i] = pack2<YT>(__uint_as_float(v[8 * q + 2 * i]), __uint_as_float(v[8 * q + 2 * i + 1]));
+                w[i] = pack2<YT>(__uint_as_float(v[c][8 * q + 2 * i]), __uint_as_float(v[c][8 * q + 2 * i + 1]));
             a[4 * c + q] = make_uint4(w[0], w[1], w[2], w[3]);
         }
-    }
 }
 
 __device__ __forceinline__ void put64(const MxGemmParams &p, uint4 (&a)[8], int row0, int n0, int k)
@@ -753,7 +747,9 @@ __global__ void __launch_bounds__(PT, 1)
                 int mb, nb;
                 tile_at(p, t, mb, nb);
                 const int count = slot_count<RK>(sl, mb);
-                if (tc > 0 && !__all_sync(0xffffffffu, pwait(p, ctl, &ctl.acc_empty, (tc - 1) & 1u))) break;
+                // the first stage is waited for before the accumulator, which comes later
+                if (!ready) ready = __all_sync(0xffffffffu, pwait(p, ctl, &ctl.full[g % GS], (g / GS) & 1u));
+                if (!ready || (tc > 0 && !__all_sync(0xffffffffu, pwait(p, ctl, &ctl.acc_empty, (tc - 1) & 1u)))) break;
                 for (int kb = 0; kb < nkb; ++kb, ++g) {
                     const int s = (int)(g % GS);
                     if (!ready && !__all_sync(0xffffffffu, pwait(p, ctl, &ctl.full[s], (g / GS) & 1u))) {
@@ -917,11 +913,25 @@ __global__ void __launch_bounds__(PT, 1)
                 }
             } else {
                 uint4 a[HC / 64][8];
+                // each piece's loads run while the one before is rounded; the accumulator goes back
+                // before the last piece is
+                uint32_t v[2][2][32];
+                tmem_ld32(tb, v[0][0]);
+                tmem_ld32(tb + 32, v[0][1]);
 #pragma unroll
-                for (int h = 0; h < HC / 64; ++h) take64<YT>(tb + 64 * h, a[h]);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(empty_bar);
+                for (int h = 0; h < HC / 64; ++h) {
+                    tmem_wait_ld32(v[h & 1][0]);
+                    tmem_wait_ld32(v[h & 1][1]);
+                    if (h + 1 < HC / 64) {
+                        tmem_ld32(tb + 64 * (h + 1), v[(h + 1) & 1][0]);
+                        tmem_ld32(tb + 64 * (h + 1) + 32, v[(h + 1) & 1][1]);
+                    } else {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(empty_bar);
+                    }
+                    round64<YT>(v[h & 1], a[h]);
+                }
 #pragma unroll
                 for (int h = 0; h < HC / 64; ++h) put64(p, a[h], row0, n0 + 64 * h, k);
             }
