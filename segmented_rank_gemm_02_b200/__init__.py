@@ -184,6 +184,8 @@ class Pool:
                "mlora_pool_create")
         self.handle = h.value
         self.d_in, self.d_out, self.n_slots, self.r_max = d_in, d_out, n_slots, r_max
+        import torch
+        self.device_index = torch.cuda.current_device()   # where the pool's memory is
 
     def load_slot(self, slot: int, rank: int, alpha: float, A, B, stream=None) -> None:
         """A: bf16 [rank, d_in], B: bf16 [d_out, rank]; numpy uint16 bits or torch tensors."""
@@ -517,8 +519,8 @@ def mx_gemm_apply(pool: Pool, segs: Optional["DeviceSegments"], X, Xq: MxMatrix,
             raise ValueError("X and Y must be on one device")
         xp, ldx = X.data_ptr(), _ld(X, "X")
         ldx = ldx if n > 1 else max(ldx, pool.d_in)
-    if Xq._index != index or W._index != index:
-        raise ValueError("Xq, W and Y must be on one device")
+    if Xq._index != index or W._index != index or pool.device_index != index:
+        raise ValueError("Xq, W and Y must be on the pool's device")
     ldy = _ld(Y, "Y")
     _call(lib().mlora_mx_gemm_apply, "mlora_mx_gemm_apply", index, stream, pool.handle,
           ctypes.byref(segs.struct) if segs is not None else None, xp, ldx, ctypes.byref(Xq.struct),
@@ -547,7 +549,7 @@ class RowGroups:
         at = self._buf.data_ptr()
         self._positions = at + 4 * (3 * S + 1 + n)
         self._out = RowGroupsStruct(at, at + 4 * (S + 1), at + 4 * (2 * S + 1), at + 4 * (3 * S + 1), self._positions)
-        self._hint, self._with_ranks, self._struct = int(max_segment_rows), with_ranks, None
+        self._hint, self._with_ranks, self._struct, self._parts = int(max_segment_rows), with_ranks, None, None
 
     def _segments(self, own_rows: bool) -> SegmentsStruct:
         o, n = self._out, self.n_tokens
@@ -564,28 +566,31 @@ class RowGroups:
         """The segments of the rows in grouped order (those of gather_rows), whatever top_k is."""
         return _GroupedSegments(self)
 
-    def _part(self, first: int, count: int):
-        return self._buf.narrow(0, first, count)
+    def _part(self, i: int):
+        if self._parts is None:
+            import torch
+            self._parts = torch.split(self._buf, (self._S + 1, self._S, self._S, self.n_tokens, self.n_tokens))
+        return self._parts[i]
 
     @property
     def offsets(self):
-        return self._part(0, self._S + 1)
+        return self._part(0)
 
     @property
     def slots(self):
-        return self._part(self._S + 1, self._S)
+        return self._part(1)
 
     @property
     def ranks(self):
-        return self._part(2 * self._S + 1, self._S)
+        return self._part(2)
 
     @property
     def order(self):
-        return self._part(3 * self._S + 1, self.n_tokens)
+        return self._part(3)
 
     @property
     def positions(self):
-        return self._part(3 * self._S + 1 + self.n_tokens, self.n_tokens)
+        return self._part(4)
 
 
 class _GroupedSegments:
@@ -605,8 +610,8 @@ def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segme
     if row_slots.dtype != torch.int32 or len(shape) not in (1, 2) or not row_slots.is_contiguous():
         raise ValueError("row_slots must be contiguous int32 [n_rows] or [n_rows, top_k]")
     n_rows, top_k, index = shape[0], 1 if len(shape) == 1 else shape[1], row_slots.get_device()
-    if top_k < 1 or index < 0:
-        raise ValueError("row_slots needs at least one slot per row, on a CUDA device")
+    if top_k < 1 or index < 0 or index != pool.device_index:
+        raise ValueError("row_slots needs at least one slot per row, on the pool's device")
     if out is None:
         out = RowGroups(pool, n_rows, top_k, None, max_segment_rows, stream, with_ranks, row_slots)
     elif out.pool is not pool or (out.n_rows, out.top_k, out._index) != (n_rows, top_k, index):

@@ -390,3 +390,80 @@ def test_rows_claimed_twice_or_missing_are_flagged():
     slot[[50, 60]] = -1
     rows = np.array([t for t in range(n) if t != 3])
     _assert_product(Y[torch.from_numpy(rows).to(DEVICE)], *_reference(slot, slot_rank, A, B, X, W, rows), d)
+
+
+@pytest.mark.parametrize("n,d_out", [(70, 136), (2600, 4104)])   # few rows, and pair tiles
+def test_infinities_stay_with_their_rows(n, d_out):
+    """An adapter with an infinity in B and an activation row with a NaN reach the rows of that
+    adapter and that row alone, although tiles mix rows of many adapters."""
+    d_in = 256
+    rng = np.random.default_rng(2)
+    slot = rng.integers(-1, 5, n).astype(np.int32)
+    bf = lambda *s: torch.from_numpy(rng.standard_normal(s) * 0.1).to(torch.bfloat16)   # noqa: E731
+    A, B = {a: bf(16, d_in) for a in range(5)}, {a: bf(d_out, 16) for a in range(5)}
+    B[3][7, 2] = float("inf")
+    pool = mlora.Pool(d_in, d_out, 5, 16)
+    for a in range(5):
+        pool.load_slot(a, 16, 2.0 * a + 1.0, A[a].to(DEVICE), B[a].to(DEVICE))
+    X, W = _rows(n, d_in, torch.bfloat16, 7, spread=1.0), _rows(d_out, d_in, torch.float32, 8, spread=1.0) * 0.05
+    nan_row = int(np.nonzero(slot == 1)[0][0])
+    clean = X.clone()
+    X[nan_row, 9] = float("nan")
+    segs = mlora.DeviceSegments(mlora.build_segments(slot, pool), n, DEVICE)
+    Xd = X.to(DEVICE)
+    Y = torch.zeros(n, d_out, dtype=torch.float32, device=DEVICE)
+    mlora.mx_gemm_apply(pool, segs, Xd, mlora.mx_quantize(Xd), mlora.mx_quantize(W.to(DEVICE)), Y)
+    assert pool.check() == 0
+    bad = ~torch.isfinite(Y).cpu().numpy()
+    want = np.zeros((n, d_out), bool)
+    want[slot == 3, 7] = True
+    want[nan_row] = True
+    assert np.array_equal(bad, want)
+    rows = np.array([t for t in range(0, n, max(1, n // 200)) if slot[t] != 3 and t != nan_row])
+    _assert_product(Y[torch.from_numpy(rows).to(DEVICE)], *_reference(slot, slot_rank_of(16, 5), A, B, clean, W, rows), d_in)
+
+
+def slot_rank_of(rank, n):
+    return np.full(n, rank, np.int32)
+
+
+def test_other_stream_and_two_pools_at_once():
+    """Two pools' products on two streams at once, each with its own workspace."""
+    cases = []
+    for seed, n in ((3, 150), (4, 300)):
+        pool, slot, slot_rank, A, B, X, W = _case(n, 512, 256, 5, (16,), 0.1, False, 100 + seed)
+        segs = mlora.DeviceSegments(mlora.build_segments(slot, pool), n, DEVICE)
+        cases.append((pool, slot, slot_rank, A, B, X, W, segs, X.to(DEVICE), mlora.mx_quantize(W.to(DEVICE)),
+                      torch.full((n, 256), float("nan"), device=DEVICE)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(5):
+        for st, (pool, _, _, _, _, _, _, segs, Xd, Wq, Y) in zip(streams, cases):
+            Xq = mlora.mx_quantize(Xd, stream=st)
+            mlora.mx_gemm_apply(pool, segs, Xd, Xq, Wq, Y, stream=st)
+    torch.cuda.synchronize()
+    for pool, slot, slot_rank, A, B, X, W, _, _, _, Y in cases:
+        assert pool.check() == 0
+        _assert_product(Y, *_reference(slot, slot_rank, A, B, X, W), 512)
+
+
+def test_a_long_matrix_passes_32_bits():
+    """Offsets past 2^32 bytes: rows near the end of a matrix of 4.3 G elements."""
+    n, d = 524300, 8192                # 8.6 GB of bf16, 2.1 GB of codes
+    X = torch.zeros(n, d, dtype=torch.bfloat16, device=DEVICE)
+    tail = _rows(40, d, torch.bfloat16, 3).to(DEVICE)
+    X[-40:] = tail
+    Q = mlora.mx_quantize(X)
+    values = mx_ref.quantize(tail.double().cpu().numpy())[2]
+    back = mlora.mx_dequantize(Q, out=X)
+    assert torch.equal(back[-40:].double().cpu(), torch.from_numpy(values)) and not back[:1000].any()
+    pool = mlora.Pool(d, 64, 1, 8)
+    W = _rows(64, d, torch.float32, 4, spread=1.0)
+    Wq = mlora.mx_quantize(W.to(DEVICE))
+    Y = torch.full((n, 64), float("nan"), dtype=torch.float32, device=DEVICE)
+    mlora.mx_gemm_apply(pool, None, None, Q, Wq, Y)
+    assert pool.check() == 0 and not Y[:-40].any()
+    w = mx_ref.quantize(W.double().numpy())[2]
+    _assert_product(Y[-40:], values @ w.T, np.abs(values) @ np.abs(w).T, np.zeros((40, 64)), d)
+    del X, Q, back, Y
+    free()

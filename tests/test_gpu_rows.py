@@ -332,3 +332,42 @@ def test_refusals_with_a_pool():
     assert gemm(segs=mlora.SegmentsStruct(1, 5, 5, 0, 256, 256, None, None, None), x=256) == bad
     assert gemm(xq=mlora.MxStruct(0, 64, 32, None, None)) == mlora.OK
     assert pool.check() == 0
+
+
+def test_rows_past_32_bits():
+    """Grouped rows whose byte offsets pass 2^32."""
+    n, k, d = 140000, 2, 8192            # 280000 grouped rows of 16 KB
+    pool = mlora.Pool(8, 8, 3, 8)
+    slots = _slots(n, k, 3, 1)
+    gr = mlora.group_rows(pool, torch.from_numpy(slots).to(DEVICE))
+    pos = gr.positions.view(n, k).long()
+    X = torch.zeros(n, d, dtype=torch.bfloat16, device=DEVICE)
+    X[:, 5] = (torch.arange(n, device=DEVICE) % 251).to(torch.bfloat16)
+    Xs = mlora.gather_rows(gr, X)
+    assert torch.equal(Xs[pos.view(-1), 5].view(n, k), X[:, 5:6].expand(n, k))
+    Y = mlora.combine_rows(gr, Xs)
+    assert torch.equal(Y[:, 5], (2 * X[:, 5].float()).to(torch.bfloat16)) and not Y[:, 6:].any()
+    dYs, dw = mlora.combine_rows_backward(gr, X, Xs, torch.ones(n, k, device=DEVICE), dYs=Xs.clone().fill_(7.0))
+    assert torch.equal(dYs[pos.view(-1), 5], Xs[pos.view(-1), 5])
+    assert torch.equal(dw, (X[:, 5:6].float() ** 2).expand(n, k))
+    assert pool.check() == 0
+    del X, Xs, Y, dYs
+    free()
+
+
+def test_streams_of_their_own():
+    """Outputs allocated for a call on another stream belong to that stream."""
+    pool = mlora.Pool(8, 8, 6, 8)
+    st = torch.cuda.Stream()
+    slots, Ys, w, dY = _operands(500, 2, 256, torch.bfloat16, 9)
+    sd, Yd, wd, dYd = (t.to(DEVICE) for t in (torch.from_numpy(slots), Ys, w, dY))
+    torch.cuda.synchronize()
+    gr = mlora.group_rows(pool, sd, stream=st)
+    Xs = mlora.gather_rows(gr, dYd, stream=st)
+    Y = mlora.combine_rows(gr, Yd, wd, stream=st)
+    dYs, dw = mlora.combine_rows_backward(gr, dYd, Yd, wd, stream=st.cuda_stream)
+    torch.cuda.synchronize()
+    _check_groups(gr, slots, 6)
+    assert torch.equal(Xs, mlora.gather_rows(gr, dYd)) and torch.equal(Y, mlora.combine_rows(gr, Yd, wd))
+    a, b = mlora.combine_rows_backward(gr, dYd, Yd, wd)
+    assert torch.equal(dYs, a) and torch.equal(dw, b)
