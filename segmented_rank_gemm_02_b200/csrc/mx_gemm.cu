@@ -74,6 +74,55 @@ __device__ __forceinline__ void store8(const MxGemmParams &p, int row, int col, 
     else store8<0>(p, row, col, f);
 }
 
+// 8 x 8 transpose of 16-byte pieces across groups of eight lanes: lane k of a group ends up with
+// piece k of the group's eight rows, so that a store instruction writes whole 128-byte lines.
+__device__ __forceinline__ void transpose8(uint4 (&a)[8], int k)
+{
+#pragma unroll
+    for (int sh = 4; sh >= 1; sh >>= 1) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j & sh) continue;
+            const bool upper = (k & sh) != 0;
+            const uint4 send = upper ? a[j] : a[j | sh];
+            uint4 recv;
+            recv.x = __shfl_xor_sync(0xffffffffu, send.x, sh);
+            recv.y = __shfl_xor_sync(0xffffffffu, send.y, sh);
+            recv.z = __shfl_xor_sync(0xffffffffu, send.z, sh);
+            recv.w = __shfl_xor_sync(0xffffffffu, send.w, sh);
+            if (upper) a[j] = recv;
+            else a[j | sh] = recv;
+        }
+    }
+}
+
+// 64 fp32 columns of this lane's row, rounded to 16 bits: eight 16-byte pieces.
+template <int YT>
+__device__ __forceinline__ void round64(const uint32_t (&v)[2][32], uint4 (&a)[8])
+{
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w[i] = pack2<YT>(__uint_as_float(v[c][8 * q + 2 * i]), __uint_as_float(v[c][8 * q + 2 * i + 1]));
+            a[4 * c + q] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+}
+
+__device__ __forceinline__ void put64(const MxGemmParams &p, uint4 (&a)[8], int row0, int n0, int k)
+{
+    transpose8(a, k);
+    const int col = n0 + 8 * k;
+    if (col >= p.d_out) return;   // d_out is a multiple of 8
+    uint16_t *y = static_cast<uint16_t *>(p.Y) + col;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        if (row0 + j < p.n_rows) *reinterpret_cast<uint4 *>(y + (int64_t)(row0 + j) * p.ldy) = a[j];
+}
+
 }  // namespace
 
 // ------------------------------------------------------------------ few rows
@@ -183,7 +232,7 @@ __device__ int4 find_rows(const TileParams &t, TileCtl &ctl, int4 *records, int 
 #pragma unroll
     for (int i = 0; i < 4; ++i) ctl.others[r][i] = 0xffffffffu;
     named_sync(kRowBar, 128);
-    if (info.x >= 0) atomicAnd(&ctl.others[slot_index(ctl.slot, info.y)][warp], ~(1u << lane));
+    if (info.x >= 0) atomicAnd(&ctl.others[slot_index(ctl.slot, total, info.y)][warp], ~(1u << lane));
     named_sync(kRowBar, 128);
     return info;
 }
@@ -386,26 +435,45 @@ __global__ void __launch_bounds__(MT, 1)
             const uint32_t tb = tmem + ((uint32_t)(32 * quarter) << 16);
             float *red = reinterpret_cast<float *>(ring) + (32 * quarter + lane) * RED_PITCH;
             const bool any = m0 + 32 * quarter < p.n_rows;   // a row of this warp exists
-            for (int c = 0; c < MC && any; c += 32) {
-                uint32_t v[32], w[32];
-                tmem_ld32(tb + c, v);
-                if (lora) tmem_ld32(tb + T_LORA + c, w);
-                tmem_wait_ld();
+            const int k = lane & 7, row0 = row - lane + 8 * (lane >> 3);
+            for (int c = 0; c < MC && any; c += 64) {
+                uint32_t v[2][32];
+                tmem_ld32(tb + c, v[0]);
+                tmem_ld32(tb + c + 32, v[1]);
                 if (lora) {
+                    uint32_t w[2][32];
+                    tmem_ld32(tb + T_LORA + c, w[0]);
+                    tmem_ld32(tb + T_LORA + c + 32, w[1]);
+                    tmem_wait_ld32(w[0]);
+                    tmem_wait_ld32(w[1]);
+                    tmem_wait_ld32(v[0]);
+                    tmem_wait_ld32(v[1]);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(w[i]));
+                    for (int i = 0; i < 32; ++i) {
+                        v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) + __uint_as_float(w[0][i]));
+                        v[1][i] = __float_as_uint(__uint_as_float(v[1][i]) + __uint_as_float(w[1][i]));
+                    }
+                } else {
+                    tmem_wait_ld32(v[0]);
+                    tmem_wait_ld32(v[1]);
                 }
-                if (row >= p.n_rows) continue;
+                if (ksplit == 1 && p.y_type != 2) {
+                    uint4 a[8];
+                    if (p.y_type == 1) round64<1>(v, a);
+                    else round64<0>(v, a);
+                    put64(p, a, row0, n0 + c, k);
+                } else if (row < p.n_rows) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float f[8];
+                    for (int q = 0; q < 8; ++q) {
+                        float f[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[8 * q + i]);
-                    if (ksplit > 1) {
-                        reinterpret_cast<float4 *>(red + c + 8 * q)[0] = make_float4(f[0], f[1], f[2], f[3]);
-                        reinterpret_cast<float4 *>(red + c + 8 * q)[1] = make_float4(f[4], f[5], f[6], f[7]);
-                    } else if (n0 + c + 8 * q < p.d_out) {   // d_out is a multiple of 8
-                        store8(p, row, n0 + c + 8 * q, f);
+                        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[q >> 2][8 * (q & 3) + i]);
+                        if (ksplit > 1) {
+                            reinterpret_cast<float4 *>(red + c + 8 * q)[0] = make_float4(f[0], f[1], f[2], f[3]);
+                            reinterpret_cast<float4 *>(red + c + 8 * q)[1] = make_float4(f[4], f[5], f[6], f[7]);
+                        } else if (n0 + c + 8 * q < p.d_out) {   // d_out is a multiple of 8
+                            store8<2>(p, row, n0 + c + 8 * q, f);
+                        }
                     }
                 }
             }
@@ -553,55 +621,6 @@ __device__ __forceinline__ int slot_count(const MxSlots &sl, int mb)
 }
 
 __device__ __forceinline__ uint32_t leader_bar(const uint64_t *bar) { return map_to_rank(smem_addr(bar), 0); }
-
-// 8 x 8 transpose of 16-byte pieces across groups of eight lanes: lane k of a group ends up with
-// piece k of the group's eight rows, so that a store instruction writes whole 128-byte lines.
-__device__ __forceinline__ void transpose8(uint4 (&a)[8], int k)
-{
-#pragma unroll
-    for (int sh = 4; sh >= 1; sh >>= 1) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (j & sh) continue;
-            const bool upper = (k & sh) != 0;
-            const uint4 send = upper ? a[j] : a[j | sh];
-            uint4 recv;
-            recv.x = __shfl_xor_sync(0xffffffffu, send.x, sh);
-            recv.y = __shfl_xor_sync(0xffffffffu, send.y, sh);
-            recv.z = __shfl_xor_sync(0xffffffffu, send.z, sh);
-            recv.w = __shfl_xor_sync(0xffffffffu, send.w, sh);
-            if (upper) a[j] = recv;
-            else a[j | sh] = recv;
-        }
-    }
-}
-
-// 64 fp32 columns of this lane's row, rounded to 16 bits: eight 16-byte pieces.
-template <int YT>
-__device__ __forceinline__ void round64(const uint32_t (&v)[2][32], uint4 (&a)[8])
-{
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                w[i] = pack2<YT>(__uint_as_float(v[c][8 * q + 2 * i]), __uint_as_float(v[c][8 * q + 2 * i + 1]));
-            a[4 * c + q] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-}
-
-__device__ __forceinline__ void put64(const MxGemmParams &p, uint4 (&a)[8], int row0, int n0, int k)
-{
-    transpose8(a, k);
-    const int col = n0 + 8 * k;
-    if (col >= p.d_out) return;   // d_out is a multiple of 8
-    uint16_t *y = static_cast<uint16_t *>(p.Y) + col;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        if (row0 + j < p.n_rows) *reinterpret_cast<uint4 *>(y + (int64_t)(row0 + j) * p.ldy) = a[j];
-}
 
 }  // namespace
 
@@ -880,7 +899,7 @@ __global__ void __launch_bounds__(PT, 1)
                     }
                     fence_proxy_async_smem();
                     named_sync(kEpiBar, 256);
-                    if (its_slot >= 0) atomicAnd(&ctl.others[slot_index(ctl.slot, its_slot)][i >> 5], ~(1u << (i & 31)));
+                    if (its_slot >= 0) atomicAnd(&ctl.others[slot_index(ctl.slot, count, its_slot)][i >> 5], ~(1u << (i & 31)));
                     named_sync(kEpiBar, 256);
                     if (i == 0) {
                         mbar_arrive(&ctl.listed);

@@ -141,10 +141,23 @@ __device__ __forceinline__ SegmentTable copy_segments(const TileParams &p, int4 
     SegmentTable t{p.n_segments < capacity ? records : nullptr, p.n_segments};
     if (t.records == nullptr && !reporter) return t;
     for (int g = tid; g < p.n_segments; g += threads) {
+        // two rounds of loads, each all at once (segment_problem's come one after the other)
         const int p0 = p.offsets[g], p1 = p.offsets[g + 1], a = p.slots[g];
-        int rank = 0;
-        float scale = 0.f;
-        const unsigned f = segment_problem(p, g, a, p0, p1, rank, scale);
+        const int want_rank = p.ranks ? p.ranks[g] : 0;
+        const float seg_scale = p.scales ? p.scales[g] : 0.f;
+        const uint32_t want_gen = p.generations ? p.generations[g] : 0u;
+        const int at = a >= 0 && a < p.n_slots ? a : 0;
+        const int rank = p.slot_rank[at];
+        const float scale = p.scales ? seg_scale : p.slot_scale[at];
+        const uint32_t gen = p.generations ? p.slot_gen[at] : 0u;
+        unsigned f = 0;
+        if (a < -1 || a >= p.n_slots) f = kFlagBadSlot;
+        else if (p0 < 0 || p1 < p0 || p1 > p.n_tokens) f = kFlagBadOffsets;
+        else if (a >= 0) {
+            if (gen != want_gen) f = kFlagStaleSlot;
+            else if (rank <= 0) f = kFlagSlotEmpty;
+            else if ((p.ranks && want_rank != rank) || rank_bucket(rank) == 0) f = kFlagBadRank;
+        }
         if (f && reporter) atomicOr(p.status, f);
         // (an end that differs from the next segment's beginning is no valid segment's)
         if (t.records) records[g] = make_int4(p0, f || a < 0 ? -1 : a, __float_as_int(scale), rank);
@@ -209,23 +222,35 @@ __device__ __forceinline__ bool first_with_slot(const int *slots, int r, int slo
     const unsigned same = __match_any_sync(0xffffffffu, slot);
     if (slot < 0 || (r & 31) != __ffs(same) - 1) return false;
     const int4 *v = reinterpret_cast<const int4 *>(slots);
-    for (int i = 0; i < (r & ~31) / 4; ++i) {
-        const int4 s = v[i];
-        if (s.x == slot || s.y == slot || s.z == slot || s.w == slot) return false;
+    bool found = false;
+    for (int i = 0; i < (r & ~31) / 4; i += 8) {   // a warp's 32 rows at a time
+        int4 s[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s[u] = v[i + u];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) found |= s[u].x == slot || s[u].y == slot || s[u].z == slot || s[u].w == slot;
     }
-    return true;
+    return !found;
 }
 
-// Index of a slot in a list of distinct slots (16-byte aligned, in shared memory) that holds it.
-__device__ __forceinline__ int slot_index(const int *list, int slot)
+// Index of a slot in a list of `count` distinct slots that holds it (in shared memory, 16-byte
+// aligned, with room for a multiple of 16).
+__device__ __forceinline__ int slot_index(const int *list, int count, int slot)
 {
     const int4 *v = reinterpret_cast<const int4 *>(list);
-    for (int i = 0; i < 2 * kOperandRows / 4; ++i) {
-        const int4 s = v[i];
-        if (s.x == slot) return 4 * i;
-        if (s.y == slot) return 4 * i + 1;
-        if (s.z == slot) return 4 * i + 2;
-        if (s.w == slot) return 4 * i + 3;
+    for (int i = 0; 4 * i < count; i += 4) {
+        int4 s[4];
+        int at = -1;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[u] = v[i + u];
+#pragma unroll
+        for (int u = 3; u >= 0; --u) {   // the first match wins (entries past the count may be anything)
+            if (s[u].w == slot) at = 4 * u + 3;
+            if (s[u].z == slot) at = 4 * u + 2;
+            if (s[u].y == slot) at = 4 * u + 1;
+            if (s[u].x == slot) at = 4 * u;
+        }
+        if (at >= 0) return 4 * i + at;
     }
     return 0;
 }
