@@ -285,10 +285,6 @@ __global__ void __launch_bounds__(MT, 1)
     // this CTA's K blocks and adapter slots
     const int nkb = (p.d_in + KB - 1) / KB;
     const int kb0 = nkb * crank / ksplit, kb1 = nkb * (crank + 1) / ksplit;
-    // While earlier kernels finish: the weights' way into L2 (a copy of what they hold later is made
-    // only after the wait).
-    if (warp == 0 && mb == 0)
-        for (int kb = kb0 + lane; kb < kb1; kb += 32) tma_prefetch_2d(&p.w_map, kb * (KB / 2), n0);
     griddep_wait();   // from here on: what earlier kernels wrote
     const uint32_t tmem = ctl.tmem;
 

@@ -490,14 +490,6 @@ __device__ __forceinline__ void tma_load_2d(void *dst_smem, const void *map, int
         : "memory");
 }
 
-// The tile of tma_load_2d into L2 only.
-__device__ __forceinline__ void tma_prefetch_2d(const void *map, int c0, int r0)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];"
-                 ::"l"(map), "r"(c0), "r"(r0)
-                 : "memory");
-}
-
 // The descriptor itself, before its first use.
 __device__ __forceinline__ void prefetch_map(const void *map)
 {
