@@ -38,7 +38,8 @@ struct mlora_pool {
     std::vector<uint32_t> h_gen;
     float *ws;              // H partial sums of the long-segment kernels (grown on demand)
     size_t ws_bytes;
-    std::vector<float *> ws_old;   // outgrown ones
+    float *ws_old[64];      // outgrown ones (each at least twice the one before)
+    int n_ws_old;
     std::mutex ws_mutex;
     // TMA views of the B blocks for rank buckets 8, 16, 32, 64 (those <= r_bucket_max):
     // one load brings one 128-column chunk of one slot's B, all its rank groups
@@ -241,7 +242,7 @@ mlora_status ensure_workspace(mlora_pool *pool, size_t bytes, cudaStream_t strea
         return MLORA_ERR_OUT_OF_MEMORY;
     }
     // The old buffer is kept: a captured graph may hold its address.
-    if (pool->ws) pool->ws_old.push_back(pool->ws);
+    if (pool->ws) pool->ws_old[pool->n_ws_old++] = pool->ws;
     pool->ws = fresh;
     pool->ws_bytes = want;
     return MLORA_OK;
@@ -453,6 +454,7 @@ mlora_status mlora_pool_create(int32_t d_in, int32_t d_out, int32_t n_slots, int
     pool->d_status = nullptr;
     pool->ws = nullptr;
     pool->ws_bytes = 0;
+    pool->n_ws_old = 0;
     pool->h_rank.assign(n_slots, 0);
     pool->h_alpha.assign(n_slots, 0.f);
     pool->h_gen.assign(n_slots, 0u);
@@ -506,7 +508,7 @@ mlora_status mlora_pool_destroy(mlora_pool *pool)
     if (pool->d_status) cudaFree(pool->d_status);
     if (pool->ws) {   // stream-ordered allocations: freed the same way, then waited for
         cudaFreeAsync(pool->ws, nullptr);
-        for (float *old : pool->ws_old) cudaFreeAsync(old, nullptr);
+        for (int i = 0; i < pool->n_ws_old; ++i) cudaFreeAsync(pool->ws_old[i], nullptr);
         cudaDeviceSynchronize();
     }
     delete pool;
