@@ -126,6 +126,47 @@ __device__ __forceinline__ uint8_t *scale_vec(const MxRows &q, int row0, int chu
     return q.scales + ((int64_t)(row0 / kTileRowsMx) * 2 * q.chunks + 2 * chunk + half) * 512 + (row0 % 32) * 16;
 }
 
+// A magnitude's own 16 bits as those of the fp32 it converts to.
+__device__ __forceinline__ uint32_t magnitude_bits(__nv_bfloat16, uint32_t m) { return m << 16; }
+__device__ __forceinline__ uint32_t magnitude_bits(__half, uint32_t m)
+{
+    return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+}
+
+// The largest magnitude of each row's block of 32 (four lanes), as fp32 bits: NaN above infinity
+// above the rest.  16-bit types compare their own bits, two elements or two rows at a time.
+template <typename T>
+__device__ __forceinline__ void block_maxima(const Eight<T> (&x)[4], uint32_t (&big)[4])
+{
+    if constexpr (sizeof(T) == 2) {
+        uint32_t m[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const uint4 v = x[u].v;
+            m[u] = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu), __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+        }
+#pragma unroll
+        for (int u = 0; u < 4; u += 2) {
+            uint32_t p = __vmaxu2(__byte_perm(m[u], m[u + 1], 0x5410), __byte_perm(m[u], m[u + 1], 0x7632));
+            p = __vmaxu2(p, __shfl_xor_sync(0xffffffffu, p, 1));
+            p = __vmaxu2(p, __shfl_xor_sync(0xffffffffu, p, 2));
+            big[u] = magnitude_bits(T(), p & 0xffffu);
+            big[u + 1] = magnitude_bits(T(), p >> 16);
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            float f[8];
+            x[u].get(f);
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            big[u] = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        }
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kQuantThreads) mx_quantize_kernel(const T *X, int64_t ldx, const MxRows q)
 {
@@ -141,19 +182,17 @@ __global__ void __launch_bounds__(kQuantThreads) mx_quantize_kernel(const T *X, 
         if (row < q.n_rows && col < q.n_cols) x[u].load(X + row * ldx + col);
         else x[u].zero();
     }
-    uint32_t words[4];   // per row: the scale bytes of this half's four blocks
+    uint32_t big[4];
+    block_maxima(x, big);
+    uint32_t bytes = 0;   // this block's scale bytes, one per row
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
+        const bool finite = big[u] < 0x7f800000u;
+        const int field = (int)(big[u] >> 23);
+        const uint32_t s = finite ? (uint32_t)max(field - 2, 0) : 255u;
+        bytes |= s << (8 * u);
         float f[8];
         x[u].get(f);
-        uint32_t big = 0;   // largest magnitude, as bits: NaN above infinity above the rest
-#pragma unroll
-        for (int i = 0; i < 8; ++i) big = max(big, __float_as_uint(f[i]) & 0x7fffffffu);
-        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const bool finite = big < 0x7f800000u;
-        const int field = (int)(big >> 23);
-        const uint32_t s = finite ? (uint32_t)max(field - 2, 0) : 255u;
         // 2^-e; a block that is not finite gets zero codes
         const float inv = finite ? __uint_as_float((254u - s) << 23) : 0.f;
         uint32_t c = 0;
@@ -163,14 +202,15 @@ __global__ void __launch_bounds__(kQuantThreads) mx_quantize_kernel(const T *X, 
         const int row = row0 + 32 * u;
         if (row < q.n_rows && col < (q.n_cols + 31) / 32 * 32)
             *reinterpret_cast<uint32_t *>(q.codes + row * q.ld + col / 2) = c;
-        uint32_t w = s << (8 * ((lane >> 2) & 3));
-        w |= __shfl_xor_sync(0xffffffffu, w, 4);
-        w |= __shfl_xor_sync(0xffffffffu, w, 8);
-        words[u] = w;
     }
-    if ((lane & 15) == 0)
-        *reinterpret_cast<uint4 *>(scale_vec(q, row0, chunk, lane >> 4)) =
-            make_uint4(words[0], words[1], words[2], words[3]);
+    // 4 x 4 bytes, blocks x rows -> rows x blocks: lane u of each half stores row u's word
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __shfl_sync(0xffffffffu, bytes, (lane & 16) + 4 * i);
+    const int u = lane & 3;
+    const uint32_t sel = u | (u + 4) << 4;
+    const uint32_t word = __byte_perm(__byte_perm(b[0], b[1], sel), __byte_perm(b[2], b[3], sel), 0x5410);
+    if ((lane & 15) < 4) *reinterpret_cast<uint32_t *>(scale_vec(q, row0, chunk, lane >> 4) + 4 * u) = word;
 }
 
 template <typename T>
