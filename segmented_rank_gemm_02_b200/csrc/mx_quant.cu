@@ -12,8 +12,10 @@
 // blocks; scale bytes in tiles of 128 rows x 4 blocks (512 bytes) as the tensor core wants them
 // in tensor memory: row r of the tile and block b at 16 (r % 32) + 4 (r / 32) + b.  A warp
 // takes 256 columns of rows r, r + 32, r + 64, r + 96 of a tile: eight elements per lane and
-// row, all loads issued before the first is used, and the 4 x 4 scale bytes of one r stored as
-// one 16-byte vector.  HBM bound: n d (size + 17/32) bytes.
+// row, all loads issued before the first is used; the 4 x 4 scale bytes of one r are transposed
+// between the lanes and stored together.  HBM bound: n d (size + 17/32) bytes.  14336 x 4096 bf16:
+// quantise 27.4 us (0.84 of the measured copy rate; 28.6 with each row's maximum compared as fp32),
+// dequantise 25.2 (0.91).
 #include "mlora.h"
 
 #include <algorithm>
