@@ -169,8 +169,9 @@ __device__ __forceinline__ void block_maxima(const Eight<T> (&x)[4], uint32_t (&
     }
 }
 
+// (16-bit types: the 32 registers that let whole SMs of threads reside)
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads) mx_quantize_kernel(const T *X, int64_t ldx, const MxRows q)
+__global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 8 : 5) mx_quantize_kernel(const T *X, int64_t ldx, const MxRows q)
 {
     griddep_launch_dependents();   // a product of Q may set itself up meanwhile; it waits for this grid
     const int lane = threadIdx.x & 31;

@@ -80,6 +80,28 @@ def test_quantize_extremes():
     assert np.array_equal(back, values, equal_nan=True)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+def test_quantize_special_rows_beside_others(dtype):
+    # rows 32 apart are quantised together: infinities, NaN of either sign, zeros, subnormals and the
+    # largest numbers of one row leave the rows beside it alone
+    X = _rows(160, 328, dtype, seed=9, spread=3.0)
+    info = torch.finfo(dtype)
+    special = [float("inf"), float("-inf"), float("nan"), info.max, -info.max, info.smallest_normal, 2.0 ** -24, 0.0]
+    for i, v in enumerate(special):
+        X[i + 32 * (i % 4), 32 * (i % 8): 32 * (i % 8) + 32] = 0
+        X[i + 32 * (i % 4), 32 * (i % 8) + 5 * (i % 6)] = v
+    bits = torch.int32 if dtype == torch.float32 else torch.int16
+    negative_nan = X[40:41, 7:8].view(bits)
+    negative_nan.fill_(-1)               # every bit set: a NaN with its sign
+    codes, scale, values = mx_ref.quantize(X.double().numpy())
+    assert np.isnan(values).any() and (scale == 255).sum() == 4
+    Q = mlora.mx_quantize(X.to(DEVICE))
+    assert np.array_equal(Q.codes.cpu().numpy(), mx_ref.pack(codes))
+    assert np.array_equal(Q.scales.cpu().numpy(), mx_ref.tile_scales(scale))
+    back = mlora.mx_dequantize(Q, dtype=torch.float32).cpu().double().numpy()
+    assert np.array_equal(back, values, equal_nan=True)
+
+
 def test_quantize_strided_rows_and_reused_output():
     wide = _rows(70, 320, torch.bfloat16, seed=4).to(DEVICE)
     X = wide[:, 32:32 + 200]        # a slice of wider rows (32 columns in: 64 bytes)
