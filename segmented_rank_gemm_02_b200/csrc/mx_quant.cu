@@ -14,8 +14,8 @@
 // takes 256 columns of rows r, r + 32, r + 64, r + 96 of a tile: eight elements per lane and
 // row, all loads issued before the first is used; the 4 x 4 scale bytes of one r are transposed
 // between the lanes and stored together.  HBM bound: n d (size + 17/32) bytes.  14336 x 4096 bf16:
-// quantise 27.4 us (0.84 of the measured copy rate; 28.6 with each row's maximum compared as fp32),
-// dequantise 25.2 (0.91).
+// quantise 26.3 us (0.87 of the measured copy rate; 28.6 with each row's maximum compared as fp32),
+// dequantise 25.2 (0.91); 7168 x 4096 fp32: 21.4 and 26.2 (0.96 and 0.78).
 #include "mlora.h"
 
 #include <algorithm>
@@ -95,11 +95,6 @@ struct Eight<float> {
     __device__ __forceinline__ void get(float (&f)[8]) const
     {
         f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
-    }
-    static __device__ __forceinline__ void store(float *p, const float (&f)[8])
-    {
-        reinterpret_cast<float4 *>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4 *>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
     }
 };
 
@@ -217,32 +212,57 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 8 : 5) mx_quan
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kQuantThreads) mx_dequantize_kernel(const MxRows q, T *X, int64_t ldx)
+__global__ void __launch_bounds__(kQuantThreads, 8) mx_dequantize_kernel(const MxRows q, T *X, int64_t ldx)
 {
     const int lane = threadIdx.x & 31;
     int row0, chunk;
     if (!my_unit(q, ((int64_t)blockIdx.x * kQuantThreads + threadIdx.x) >> 5, row0, chunk)) return;
-    const int col = chunk * 256 + lane * 8;
-    const uint4 sv = *reinterpret_cast<const uint4 *>(scale_vec(q, row0, chunk, lane >> 4));
-    const uint32_t words[4] = {sv.x, sv.y, sv.z, sv.w};
+    // A lane's eight elements: eight columns in a row; in fp32 four, and four 128 columns on, so that a
+    // store instruction writes 512 consecutive bytes (16 of every 32 at a time: 7168 x 4096 took 37 us).
+    constexpr bool kSplit = sizeof(T) == 4;
+    constexpr int kNext = kSplit ? 128 : 4;
+    const int col = chunk * 256 + lane * (kSplit ? 4 : 8);
+    const bool in[2] = {col < q.n_cols, col + kNext < q.n_cols};   // n_cols is a multiple of 8
+    const uint4 sv = *reinterpret_cast<const uint4 *>(scale_vec(q, row0, chunk, kSplit ? 0 : lane >> 4));
+    uint4 tv = sv;
+    if (kSplit) tv = *reinterpret_cast<const uint4 *>(scale_vec(q, row0, chunk, 1));
+    const uint32_t words[2][4] = {{sv.x, sv.y, sv.z, sv.w}, {tv.x, tv.y, tv.z, tv.w}};
+    const int byte = kSplit ? lane >> 3 : (lane >> 2) & 3;
     uint32_t c[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int row = row0 + 32 * u;
-        c[u] = row < q.n_rows && col < q.n_cols ? *reinterpret_cast<const uint32_t *>(q.codes + row * q.ld + col / 2) : 0u;
+        const uint8_t *src = q.codes + row * q.ld + col / 2;
+        c[u] = 0;
+        if (row >= q.n_rows) continue;
+        if constexpr (kSplit) {
+            if (in[0]) c[u] = *reinterpret_cast<const uint16_t *>(src);
+            if (in[1]) c[u] |= (uint32_t)*reinterpret_cast<const uint16_t *>(src + kNext / 2) << 16;
+        } else {
+            if (in[0]) c[u] = *reinterpret_cast<const uint32_t *>(src);
+        }
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         const int row = row0 + 32 * u;
-        if (row >= q.n_rows || col >= q.n_cols) continue;
-        const uint32_t s = (words[u] >> (8 * ((lane >> 2) & 3))) & 0xffu;
-        // 2^(s - 127): subnormal for s = 0, NaN for 255
-        const float scale = __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
-        float f[8];
+        if (row >= q.n_rows) continue;
+        float f[8], scale[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t s = (words[h][u] >> (8 * byte)) & 0xffu;
+            // 2^(s - 127): subnormal for s = 0, NaN for 255
+            scale[h] = __uint_as_float(s == 255u ? 0x7fc00000u : s == 0u ? 0x00400000u : s << 23);
+        }
         e2m1x8_to_float(c[u], f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] *= scale;
-        Eight<T>::store(X + row * ldx + col, f);
+        for (int i = 0; i < 8; ++i) f[i] *= scale[i / 4];
+        T *y = X + row * ldx + col;
+        if constexpr (kSplit) {
+            if (in[0]) *reinterpret_cast<float4 *>(y) = make_float4(f[0], f[1], f[2], f[3]);
+            if (in[1]) *reinterpret_cast<float4 *>(y + kNext) = make_float4(f[4], f[5], f[6], f[7]);
+        } else {
+            if (in[0]) Eight<T>::store(y, f);
+        }
     }
 }
 
