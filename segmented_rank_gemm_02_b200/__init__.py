@@ -155,10 +155,13 @@ def _ptr(x) -> Optional[int]:
     return int(x)
 
 
-def _ld(t, what: str) -> int:
+def _ld(t, what: str, rows: int = 0) -> int:
+    """Row stride of a row-major operand that must have `rows` rows or more."""
     st = t.stride()
     if len(st) != 2 or st[1] != 1:
         raise ValueError(f"{what} must be a 2-D row-major tensor")
+    if t.shape[0] < rows:
+        raise ValueError(f"{what} has {t.shape[0]} rows, the segments are of {rows}")
     return int(st[0])
 
 
@@ -302,15 +305,16 @@ class DeviceSegments:
 
 def apply(pool: Pool, segs: DeviceSegments, X, Y, stream=None) -> None:
     """Y[t] = bf16(Y[t] + s (X[t] A^T) B^T) in place (mlora_apply)."""
-    _check(lib().mlora_apply(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X"),
-                            _ptr(Y), _ld(Y, "Y"), _stream_ptr(stream)), "mlora_apply")
+    _check(lib().mlora_apply(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X", segs.struct.n_rows),
+                            _ptr(Y), _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)), "mlora_apply")
 
 
 def apply_noalloc(pool: Pool, segs: DeviceSegments, X, Y, stream=None) -> None:
     """mlora_apply with the long-segment scratch in the library's fixed device array
     (mlora_apply_noalloc): allocates nothing; concurrent calls on the GPU race."""
-    _check(lib().mlora_apply_noalloc(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X"),
-                                     _ptr(Y), _ld(Y, "Y"), _stream_ptr(stream)), "mlora_apply_noalloc")
+    _check(lib().mlora_apply_noalloc(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X", segs.struct.n_rows),
+                                     _ptr(Y), _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)),
+           "mlora_apply_noalloc")
 
 
 MAX_FUSED = 4
@@ -331,7 +335,8 @@ def apply_ex(pool: Pool, segs: DeviceSegments, X, Y, x_scale: float = 1.0, strea
     """mlora_apply at a quantized base model's dtype boundary (mlora_apply_ex): X bf16 or
     FP8 e4m3 codes (value = code * x_scale), Y bf16, fp16 or fp32, updated in place."""
     _check(lib().mlora_apply_ex(pool.handle, ctypes.byref(segs.struct), _ptr(X), _dtype_code(X), float(x_scale),
-                                _ld(X, "X"), _ptr(Y), _dtype_code(Y), _ld(Y, "Y"), _stream_ptr(stream)),
+                                _ld(X, "X", segs.struct.n_rows), _ptr(Y), _dtype_code(Y),
+                                _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)),
            "mlora_apply_ex")
 
 
@@ -339,8 +344,9 @@ def base_gemm_apply(pool: Pool, segs: DeviceSegments, X, W, Y, stream=None) -> N
     """Y = bf16(X W^T + s (X A^T) B^T) for adapter rows, bf16(X W^T) for the others, in
     one pass (mlora_base_gemm_apply).  X [n_rows, d_in], W [d_out, d_in] (nn.Linear
     layout) and Y [n_rows, d_out], all bf16 on the pool's device; Y is written, not read."""
-    _check(lib().mlora_base_gemm_apply(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X"), _ptr(W),
-                                       _ld(W, "W"), _ptr(Y), _ld(Y, "Y"), _stream_ptr(stream)),
+    _check(lib().mlora_base_gemm_apply(pool.handle, ctypes.byref(segs.struct), _ptr(X),
+                                       _ld(X, "X", segs.struct.n_rows), _ptr(W), _ld(W, "W"), _ptr(Y),
+                                       _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)),
            "mlora_base_gemm_apply")
 
 
@@ -353,21 +359,21 @@ def apply_multi(pools, segs: DeviceSegments, X, Ys, stream=None) -> None:
     n = len(pools)
     handles = (ctypes.c_void_p * max(n, 1))(*[p.handle for p in pools])
     outs = (ctypes.c_void_p * max(n, 1))(*[_ptr(Y) for Y in Ys])
-    lds = (ctypes.c_int64 * max(n, 1))(*[_ld(Y, "Y") for Y in Ys])
-    _check(lib().mlora_apply_multi(handles, n, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X"),
+    lds = (ctypes.c_int64 * max(n, 1))(*[_ld(Y, "Y", segs.struct.n_rows) for Y in Ys])
+    _check(lib().mlora_apply_multi(handles, n, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X", segs.struct.n_rows),
                                    outs, lds, _stream_ptr(stream)), "mlora_apply_multi")
 
 
 def shrink(pool: Pool, segs: DeviceSegments, X, H, stream=None) -> None:
     """H[p, :r] = X[t_p] A^T, fp32, grouped order (mlora_shrink)."""
-    _check(lib().mlora_shrink(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X"),
-                             _ptr(H), _ld(H, "H"), _stream_ptr(stream)), "mlora_shrink")
+    _check(lib().mlora_shrink(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X", segs.struct.n_rows),
+                             _ptr(H), _ld(H, "H", segs.struct.n_tokens), _stream_ptr(stream)), "mlora_shrink")
 
 
 def expand(pool: Pool, segs: DeviceSegments, H, Y, stream=None) -> None:
     """Y[t_p] = bf16(Y[t_p] + s H[p, :r] B^T) in place (mlora_expand)."""
-    _check(lib().mlora_expand(pool.handle, ctypes.byref(segs.struct), _ptr(H), _ld(H, "H"),
-                             _ptr(Y), _ld(Y, "Y"), _stream_ptr(stream)), "mlora_expand")
+    _check(lib().mlora_expand(pool.handle, ctypes.byref(segs.struct), _ptr(H), _ld(H, "H", segs.struct.n_tokens),
+                             _ptr(Y), _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)), "mlora_expand")
 
 
 _float_codes = {}   # torch dtype -> MLORA_DTYPE_* of the types rows and outputs may have
