@@ -266,7 +266,8 @@ mlora_status mlora_apply_ex(mlora_pool *pool, const mlora_segments *segs, const 
  * per row and per 128 rows a list of slots) is the pool's, grown as for mlora_apply
  * (not during stream capture: MLORA_ERR_UNSUPPORTED) and shared with it.  Segments
  * that mlora_apply rejects set the same status bits here and their rows get X W^T
- * only; a row claimed by two segments keeps one claim and sets MLORA_FLAG_BAD_ROW.
+ * only; a row claimed twice keeps the claim of the lowest grouped position and sets
+ * MLORA_FLAG_BAD_ROW.
  */
 mlora_status mlora_base_gemm_apply(mlora_pool *pool, const mlora_segments *segs, const void *X, int64_t ldx,
                                    const void *W, int64_t ldw, void *Y, int64_t ldy, void *stream);

@@ -143,9 +143,9 @@ __device__ __forceinline__ uint32_t leader_bar(const uint64_t *bar) { return map
 // Grid-stride over segments (their problems are reported once each) and over
 // grouped positions: position q belongs to the segment g with offsets[g] <= q <
 // offsets[g + 1] (binary search over the offsets); when that segment is a valid
-// adapter segment, row_info[token_indices[q]] = {q, slot, scale, rank}.  A row
-// claimed twice keeps its first claim and is reported; rows of base or rejected
-// segments and uncovered rows keep position -1 (base only).
+// adapter segment, row_info[token_indices[q]].x = q.  A row claimed twice keeps the
+// lowest position, whatever the order of the claims, and is reported; rows of base or
+// rejected segments and uncovered rows keep position -1 (base only).
 __global__ void __launch_bounds__(256) row_map_kernel(const __grid_constant__ TileParams p, int4 *row_info)
 {
     const int stride = (int)(gridDim.x * blockDim.x);
@@ -157,35 +157,31 @@ __global__ void __launch_bounds__(256) row_map_kernel(const __grid_constant__ Ti
         if (f) atomicOr(p.status, f);
     }
     if (p.n_segments <= 0) return;
-    for (int q = i0; q < p.n_tokens; q += stride) {
-        const int g = segment_of_position(p, q), a = p.slots[g], p0 = p.offsets[g], p1 = p.offsets[g + 1];
-        if (a < 0 || q < p0 || q >= p1) continue;
-        int rank = 0;
-        float scale = 0.f;
-        if (segment_problem(p, g, a, p0, p1, rank, scale)) continue;
-        const int t = p.token_indices ? p.token_indices[q] : q;
-        if (t < 0 || t >= p.n_rows || atomicCAS(&row_info[t].x, -1, q) != -1) {
+    for (int64_t q = i0; q < p.n_tokens; q += stride) {
+        if (row_of_position(p, SegmentTable{nullptr, p.n_segments}, (int)q).x < 0) continue;
+        const int t = p.token_indices ? p.token_indices[q] : (int)q;
+        if (t < 0 || t >= p.n_rows ||
+            atomicMin(reinterpret_cast<unsigned *>(&row_info[t].x), (unsigned)q) != kUnclaimed)
             atomicOr(p.status, kFlagBadRow);
-            continue;
-        }
-        row_info[t].y = a;
-        row_info[t].z = __float_as_int(scale);
-        row_info[t].w = rank;
     }
 }
 
-// One CTA of 256 threads per 256-row block: the distinct slots of the block's rows in
-// order of first appearance, as out[0] = count, then (slot, rank bucket) pairs.
-__global__ void __launch_bounds__(PM) block_slots_kernel(const int4 *row_info, int n_rows, int32_t *out)
+// One CTA of 256 threads per 256-row block, after row_map_kernel: completes its rows'
+// row_info = {q, slot, scale, rank} and lists the block's distinct slots in order of first
+// appearance, as out[0] = count, then (slot, rank bucket) pairs.
+__global__ void __launch_bounds__(PM)
+    block_slots_kernel(const __grid_constant__ TileParams p, int4 *row_info, int32_t *out)
 {
     __shared__ int s_slot[PM];
     __shared__ int s_count[PM / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int row = blockIdx.x * PM + tid;
     int slot = -1, rank = 0;
-    if (row < n_rows) {
-        const int4 v = row_info[row];
-        if (v.x >= 0) {
+    if (row < p.n_rows) {
+        const int q = row_info[row].x;
+        if (q >= 0) {
+            const int4 v = row_of_position(p, SegmentTable{nullptr, p.n_segments}, q);
+            row_info[row] = v;
             slot = v.y;
             rank = v.w;
         }
@@ -585,11 +581,11 @@ cudaError_t launch_row_map(const TileParams &p, int4 *row_info, cudaStream_t str
     return cudaGetLastError();
 }
 
-cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream)
+cudaError_t launch_block_slots(const TileParams &p, int4 *row_info, int32_t *block_slots, cudaStream_t stream)
 {
-    const int n_mblk = (n_rows + PM - 1) / PM;
+    const int n_mblk = (p.n_rows + PM - 1) / PM;
     if (n_mblk <= 0) return cudaSuccess;
-    block_slots_kernel<<<n_mblk, PM, 0, stream>>>(row_info, n_rows, block_slots);
+    block_slots_kernel<<<n_mblk, PM, 0, stream>>>(p, row_info, block_slots);
     return cudaGetLastError();
 }
 
@@ -605,7 +601,7 @@ cudaError_t launch_row_blocks(const TileParams &p, int4 *row_info, int32_t *bloc
         return cudaGetLastError();
     }
     const cudaError_t e = launch_row_map(p, row_info, stream);
-    return e != cudaSuccess ? e : launch_block_slots(row_info, p.n_rows, block_slots, stream);
+    return e != cudaSuccess ? e : launch_block_slots(p, row_info, block_slots, stream);
 }
 
 namespace {

@@ -203,11 +203,11 @@ struct GemmParams {
     int32_t n_rows, d_in, d_out, n_mblk, n_nblk;
 };
 
-// row_info for every row (memset to -1, then the valid segments' rows); reports the
-// segments' problems in p.status.
+// Every row's grouped position in row_info (memset to -1, then the valid segments' rows); reports
+// the segments' problems in p.status.
 cudaError_t launch_row_map(const TileParams &p, int4 *row_info, cudaStream_t stream);
-// The distinct slots of each 256-row block of rows.
-cudaError_t launch_block_slots(const int4 *row_info, int n_rows, int32_t *block_slots, cudaStream_t stream);
+// After it: the rest of row_info, and the distinct slots of each 256-row block of rows.
+cudaError_t launch_block_slots(const TileParams &p, int4 *row_info, int32_t *block_slots, cudaStream_t stream);
 // Both, in one launch where the list of grouped positions is short.
 cudaError_t launch_row_blocks(const TileParams &p, int4 *row_info, int32_t *block_slots, cudaStream_t stream);
 // Tile width (256 or 512 columns of Y) for n_mblk 256-row blocks and d_out columns.

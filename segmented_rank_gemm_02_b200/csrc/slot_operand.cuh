@@ -189,8 +189,12 @@ __device__ __forceinline__ int4 row_of_position(const TileParams &p, const Segme
     return make_int4(q, a, __float_as_int(scale), rank);
 }
 
-// Finds the rows of a block [row0, row0 + n): claims[r] (preset to -1) gets the grouped position that
-// names row r and lies in a valid adapter segment.  A row claimed twice keeps one claim and is flagged;
+// A row that nothing has claimed (as unsigned, so that every grouped position is below it).
+constexpr unsigned kUnclaimed = 0xffffffffu;
+
+// Finds the rows of a block [row0, row0 + n): claims[r] (preset to -1, that is kUnclaimed) gets the lowest
+// grouped position that names row r and lies in a valid adapter segment, whatever the order of the
+// claims, so that all CTAs that look the same rows up agree.  A row claimed twice is flagged;
 // `reporter` flags rows that do not exist.
 __device__ __forceinline__ void claim_rows(const TileParams &p, const SegmentTable &t, int row0, int n, int *claims,
                                            int tid, int threads, bool reporter)
@@ -210,7 +214,8 @@ __device__ __forceinline__ void claim_rows(const TileParams &p, const SegmentTab
             const bool in = exists && row[u] >= row0 && row[u] < row0 + n;
             if (!in && !(reporter && !exists)) continue;
             if (row_of_position(p, t, (int)q).x < 0) continue;
-            if (!in || atomicCAS(&claims[row[u] - row0], -1, (int)q) != -1) atomicOr(p.status, kFlagBadRow);
+            if (!in || atomicMin(reinterpret_cast<unsigned *>(&claims[row[u] - row0]), (unsigned)q) != kUnclaimed)
+                atomicOr(p.status, kFlagBadRow);
         }
     }
 }
