@@ -535,8 +535,9 @@ def mx_gemm_apply(pool: Pool, segs: Optional["DeviceSegments"], X, Xq: MxMatrix,
 
 class RowGroups:
     """Rows grouped by slot on the device (mlora_group_rows), usable as DeviceSegments: of the
-    batch's own rows with one slot per row, of the rows in grouped order (gather_rows) with more
-    (grouped() gives the latter in either case).
+    batch's own rows if they were grouped by row_slots [n_rows], of the rows in grouped order
+    (gather_rows) if by [n_rows, top_k], [n_rows, 1] among them.  grouped() gives the latter in
+    either case.
 
     offsets, slots, ranks, order, positions: int32 device tensors (see mlora.h).  ranks are this pool's;
     with_ranks=False leaves them out of the segments, for use with pools whose ranks differ."""
@@ -556,6 +557,7 @@ class RowGroups:
         self._positions = at + 4 * (3 * S + 1 + n)
         self._out = RowGroupsStruct(at, at + 4 * (S + 1), at + 4 * (2 * S + 1), at + 4 * (3 * S + 1), self._positions)
         self._hint, self._with_ranks, self._struct, self._parts = int(max_segment_rows), with_ranks, None, None
+        self._own_rows = top_k == 1   # until group_rows sees the shape of its row_slots
 
     def _segments(self, own_rows: bool) -> SegmentsStruct:
         o, n = self._out, self.n_tokens
@@ -565,11 +567,11 @@ class RowGroups:
     @property
     def struct(self) -> SegmentsStruct:
         if self._struct is None:
-            self._struct = self._segments(self.top_k == 1)
+            self._struct = self._segments(self._own_rows)
         return self._struct
 
     def grouped(self) -> "_GroupedSegments":
-        """The segments of the rows in grouped order (those of gather_rows), whatever top_k is."""
+        """The segments of the rows in grouped order (those of gather_rows), whatever was grouped."""
         return _GroupedSegments(self)
 
     def _part(self, i: int):
@@ -608,7 +610,8 @@ class _GroupedSegments:
 def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segment_rows: int = 0,
                stream=None, with_ranks: bool = True) -> RowGroups:
     """Sort rows by adapter slot on the device (mlora_group_rows).  row_slots: int32 [n_rows] or
-    [n_rows, top_k], contiguous, -1 = base model.  `out` reuses a RowGroups of the same sizes (a
+    [n_rows, top_k], contiguous, -1 = base model; which of the two decides what the result is as
+    segments (see RowGroups).  `out` reuses a RowGroups of the same sizes (a
     captured graph's).  max_segment_rows: the hint of mlora_segments, if the caller knows one;
     with_ranks: see RowGroups (both only without `out`)."""
     import torch
@@ -624,6 +627,8 @@ def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segme
         raise ValueError("out must be of this pool, the same sizes and device")
     _call(lib().mlora_group_rows, "mlora_group_rows", index, stream, pool.handle, row_slots.data_ptr(), n_rows, top_k,
           ctypes.byref(out._out))
+    if out._own_rows != (len(shape) == 1):
+        out._own_rows, out._struct = len(shape) == 1, None
     return out
 
 
