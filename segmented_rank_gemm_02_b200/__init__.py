@@ -298,21 +298,31 @@ class DeviceSegments:
             _ptr(self.offsets), _ptr(self.slots), _ptr(self.ranks), _ptr(self.scales),
             _ptr(self.token_indices), _ptr(self.generations))
 
+        self._index = self.offsets.get_device()
+
     @property
     def n_tokens(self) -> int:
         return int(self.struct.n_tokens)
 
 
+def _seg_ref(pool: Pool, segs):
+    """The segments' struct for a call on the pool; their arrays must be where its kernels read them."""
+    index = getattr(segs, "_index", None)
+    if index is not None and index != pool.device_index and segs.struct.n_segments > 0:
+        raise ValueError("the segments must be on the pool's device")
+    return ctypes.byref(segs.struct)
+
+
 def apply(pool: Pool, segs: DeviceSegments, X, Y, stream=None) -> None:
     """Y[t] = bf16(Y[t] + s (X[t] A^T) B^T) in place (mlora_apply)."""
-    _check(lib().mlora_apply(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X", segs.struct.n_rows),
+    _check(lib().mlora_apply(pool.handle, _seg_ref(pool, segs), _ptr(X), _ld(X, "X", segs.struct.n_rows),
                             _ptr(Y), _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)), "mlora_apply")
 
 
 def apply_noalloc(pool: Pool, segs: DeviceSegments, X, Y, stream=None) -> None:
     """mlora_apply with the long-segment scratch in the library's fixed device array
     (mlora_apply_noalloc): allocates nothing; concurrent calls on the GPU race."""
-    _check(lib().mlora_apply_noalloc(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X", segs.struct.n_rows),
+    _check(lib().mlora_apply_noalloc(pool.handle, _seg_ref(pool, segs), _ptr(X), _ld(X, "X", segs.struct.n_rows),
                                      _ptr(Y), _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)),
            "mlora_apply_noalloc")
 
@@ -334,7 +344,7 @@ def _dtype_code(t) -> int:
 def apply_ex(pool: Pool, segs: DeviceSegments, X, Y, x_scale: float = 1.0, stream=None) -> None:
     """mlora_apply at a quantized base model's dtype boundary (mlora_apply_ex): X bf16 or
     FP8 e4m3 codes (value = code * x_scale), Y bf16, fp16 or fp32, updated in place."""
-    _check(lib().mlora_apply_ex(pool.handle, ctypes.byref(segs.struct), _ptr(X), _dtype_code(X), float(x_scale),
+    _check(lib().mlora_apply_ex(pool.handle, _seg_ref(pool, segs), _ptr(X), _dtype_code(X), float(x_scale),
                                 _ld(X, "X", segs.struct.n_rows), _ptr(Y), _dtype_code(Y),
                                 _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)),
            "mlora_apply_ex")
@@ -344,7 +354,7 @@ def base_gemm_apply(pool: Pool, segs: DeviceSegments, X, W, Y, stream=None) -> N
     """Y = bf16(X W^T + s (X A^T) B^T) for adapter rows, bf16(X W^T) for the others, in
     one pass (mlora_base_gemm_apply).  X [n_rows, d_in], W [d_out, d_in] (nn.Linear
     layout) and Y [n_rows, d_out], all bf16 on the pool's device; Y is written, not read."""
-    _check(lib().mlora_base_gemm_apply(pool.handle, ctypes.byref(segs.struct), _ptr(X),
+    _check(lib().mlora_base_gemm_apply(pool.handle, _seg_ref(pool, segs), _ptr(X),
                                        _ld(X, "X", segs.struct.n_rows), _ptr(W), _ld(W, "W"), _ptr(Y),
                                        _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)),
            "mlora_base_gemm_apply")
@@ -357,6 +367,8 @@ def apply_multi(pools, segs: DeviceSegments, X, Ys, stream=None) -> None:
     if len(pools) != len(Ys):
         raise ValueError("one output per pool")
     n = len(pools)
+    for p in pools:
+        _seg_ref(p, segs)
     handles = (ctypes.c_void_p * max(n, 1))(*[p.handle for p in pools])
     outs = (ctypes.c_void_p * max(n, 1))(*[_ptr(Y) for Y in Ys])
     lds = (ctypes.c_int64 * max(n, 1))(*[_ld(Y, "Y", segs.struct.n_rows) for Y in Ys])
@@ -366,13 +378,13 @@ def apply_multi(pools, segs: DeviceSegments, X, Ys, stream=None) -> None:
 
 def shrink(pool: Pool, segs: DeviceSegments, X, H, stream=None) -> None:
     """H[p, :r] = X[t_p] A^T, fp32, grouped order (mlora_shrink)."""
-    _check(lib().mlora_shrink(pool.handle, ctypes.byref(segs.struct), _ptr(X), _ld(X, "X", segs.struct.n_rows),
+    _check(lib().mlora_shrink(pool.handle, _seg_ref(pool, segs), _ptr(X), _ld(X, "X", segs.struct.n_rows),
                              _ptr(H), _ld(H, "H", segs.struct.n_tokens), _stream_ptr(stream)), "mlora_shrink")
 
 
 def expand(pool: Pool, segs: DeviceSegments, H, Y, stream=None) -> None:
     """Y[t_p] = bf16(Y[t_p] + s H[p, :r] B^T) in place (mlora_expand)."""
-    _check(lib().mlora_expand(pool.handle, ctypes.byref(segs.struct), _ptr(H), _ld(H, "H", segs.struct.n_tokens),
+    _check(lib().mlora_expand(pool.handle, _seg_ref(pool, segs), _ptr(H), _ld(H, "H", segs.struct.n_tokens),
                              _ptr(Y), _ld(Y, "Y", segs.struct.n_rows), _stream_ptr(stream)), "mlora_expand")
 
 
@@ -529,7 +541,7 @@ def mx_gemm_apply(pool: Pool, segs: Optional["DeviceSegments"], X, Xq: MxMatrix,
         raise ValueError("Xq, W and Y must be on the pool's device")
     ldy = _ld(Y, "Y")
     _call(lib().mlora_mx_gemm_apply, "mlora_mx_gemm_apply", index, stream, pool.handle,
-          ctypes.byref(segs.struct) if segs is not None else None, xp, ldx, ctypes.byref(Xq.struct),
+          _seg_ref(pool, segs) if segs is not None else None, xp, ldx, ctypes.byref(Xq.struct),
           ctypes.byref(W.struct), Y.data_ptr(), _float_code(Y, "Y"), ldy if n > 1 else max(ldy, pool.d_out))
 
 
@@ -603,7 +615,7 @@ class RowGroups:
 
 class _GroupedSegments:
     def __init__(self, groups: RowGroups):
-        self.groups, self.n_tokens = groups, groups.n_tokens   # (keeps the arrays)
+        self.groups, self.n_tokens, self._index = groups, groups.n_tokens, groups._index   # (keeps the arrays)
         self.struct = groups._segments(False)
 
 

@@ -46,3 +46,23 @@ def test_operands_shorter_than_the_segments_are_refused(mlora, call, short):
     H = torch.zeros(rows["H"], 16)
     with pytest.raises(ValueError, match=f"{short} has 6 rows"):
         _calls(mlora, pool, segs, X, Y, H)[call]()
+
+
+@pytest.mark.parametrize("call", ["apply", "apply_noalloc", "apply_ex", "base_gemm_apply", "apply_multi", "shrink",
+                                  "expand", "mx_gemm_apply"])
+def test_segments_elsewhere_are_refused(mlora, call):
+    """Segments whose arrays are not on the pool's device (here: in host memory) would be read by its kernels
+    all the same."""
+    meta = {"offsets": [0, 2, 4], "slots": [0, 1], "token_indices": [3, 1, 0, 2]}
+    pool = SimpleNamespace(handle=None, d_in=8, d_out=16, n_slots=2, device_index=-2)   # no tensor is there
+    groups = mlora.RowGroups(pool, 4, 1, "cpu")
+    X, Y, H = torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(4, 16, dtype=torch.bfloat16), torch.zeros(4, 16)
+    for segs in (mlora.DeviceSegments(meta, 4, "cpu"), groups, groups.grouped()):
+        calls = _calls(mlora, pool, segs, X, Y, H)
+        calls["mx_gemm_apply"] = lambda segs=segs: mlora.mx_gemm_apply(
+            SimpleNamespace(handle=None, d_in=8, d_out=16, device_index=-1), segs, X, mlora.MxMatrix(4, 8, "cpu"),
+            mlora.MxMatrix(16, 8, "cpu"), Y)
+        if call == "mx_gemm_apply":
+            segs._index = 0   # the matrices' device is looked at first
+        with pytest.raises(ValueError, match="segments must be on the pool's device"):
+            calls[call]()
