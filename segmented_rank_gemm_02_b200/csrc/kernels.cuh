@@ -228,7 +228,8 @@ struct MxGemmParams {
                                 // 128-byte swizzle
     CUtensorMap xs_map, ws_map; // scale tiles as 32-bit words [128-row blocks][256 per 256 columns], box 256 x
                                 // the blocks of a tile
-    CUtensorMap b_map[4];       // the pool's B blocks, as in GemmParams
+    CUtensorMap b_map[4];       // the pool's B blocks, as in GemmParams: those of buckets up to
+    int32_t rank_bucket_max;    // the pool's largest (0 without LoRA)
     int32_t b_col_div;
     void *Y;                    // [n_rows][ldy], written for every row
     int64_t ldy;
@@ -261,13 +262,11 @@ struct MxPlan {
 };
 MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out);
 
-// Y = X W^T (+ the slots' low-rank products if rank_bucket_max > 0, the pool's largest bucket).
+// Y = X W^T (+ the slots' low-rank products if p.rank_bucket_max > 0).
 // Both launch with programmatic dependent launch: they read nothing before the kernels that the
 // one before them in the stream waited for, and that one itself, are complete.
-cudaError_t launch_mx_tile(const MxGemmParams &p, const MxSegments &sg, int rank_bucket_max, int ksplit,
-                           cudaStream_t stream);
-cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int rank_bucket_max, int cols,
-                           cudaStream_t stream);
+cudaError_t launch_mx_tile(const MxGemmParams &p, const MxSegments &sg, int ksplit, cudaStream_t stream);
+cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int cols, cudaStream_t stream);
 cudaError_t prepare_mx_gemm();
 
 // ---- rows grouped by slot (rows.cu)

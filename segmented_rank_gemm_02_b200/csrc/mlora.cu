@@ -804,10 +804,11 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
     g.n_mblk = (Xq->n_rows + plan.rows - 1) / plan.rows;
     g.n_nblk = (pool->d_out + plan.cols - 1) / plan.cols;
     if (!lora) {
-        const cudaError_t e = few ? mlora::launch_mx_tile(g, mlora::MxSegments{}, 0, plan.ksplit, cs)
-                                  : mlora::launch_mx_pair(g, mlora::MxSlots{}, 0, plan.cols, cs);
+        const cudaError_t e = few ? mlora::launch_mx_tile(g, mlora::MxSegments{}, plan.ksplit, cs)
+                                  : mlora::launch_mx_pair(g, mlora::MxSlots{}, plan.cols, cs);
         return e == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
     }
+    g.rank_bucket_max = pool->r_bucket_max;
     for (int i = 0; i < 4; ++i) {
         g.b_map[i] = pool->b_maps_wide_ok ? pool->b_maps_wide[i] : pool->b_maps[i];
         if (b_cols != 128 && (8 << i) <= pool->r_bucket_max &&
@@ -838,9 +839,9 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
     st = launch(pool, segs, mlora::MODE_SHRINK, p, stream);
     if (st != MLORA_OK) return st;
     const cudaError_t e =
-        few ? mlora::launch_mx_tile(g, mlora::MxSegments{p, H, rk}, pool->r_bucket_max, plan.ksplit, cs)
+        few ? mlora::launch_mx_tile(g, mlora::MxSegments{p, H, rk}, plan.ksplit, cs)
             : mlora::launch_mx_pair(g, mlora::MxSlots{row_info, block_slots, H, rk, long_path(pool, segs) ? 1 : 0},
-                                     pool->r_bucket_max, plan.cols, cs);
+                                     plan.cols, cs);
     return e == cudaSuccess ? MLORA_OK : MLORA_ERR_CUDA;
 }
 

@@ -262,7 +262,8 @@ __global__ void __launch_bounds__(MT, 1)
         tmem_relinquish();
     }
     if (tid < 4) prefetch_map(tid == 0 ? &p.w_map : tid == 1 ? &p.x_map : tid == 2 ? &p.ws_map : &p.xs_map);
-    if (RK > 0 && tid >= 4 && tid < 8 && 8 << (tid - 4) <= RK) prefetch_map(&p.b_map[tid - 4]);
+    // (the maps past the pool's largest bucket are not encoded)
+    if (RK > 0 && tid >= 4 && tid < 8 && 8 << (tid - 4) <= p.rank_bucket_max) prefetch_map(&p.b_map[tid - 4]);
     if (tid == 0) {
         for (int s = 0; s < GS; ++s) {
             mbar_init(&ctl.full[s], 1);
@@ -1097,23 +1098,21 @@ MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
     return plan;
 }
 
-cudaError_t launch_mx_tile(const MxGemmParams &p, const MxSegments &sg, int rank_bucket_max, int ksplit,
-                           cudaStream_t stream)
+cudaError_t launch_mx_tile(const MxGemmParams &p, const MxSegments &sg, int ksplit, cudaStream_t stream)
 {
-    if (rank_bucket_max == 0) return launch_tile<0>(p, sg, ksplit, stream);
-    if (rank_bucket_max <= 16) return launch_tile<16>(p, sg, ksplit, stream);
+    if (p.rank_bucket_max == 0) return launch_tile<0>(p, sg, ksplit, stream);
+    if (p.rank_bucket_max <= 16) return launch_tile<16>(p, sg, ksplit, stream);
     return launch_tile<64>(p, sg, ksplit, stream);
 }
 
-cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int rank_bucket_max, int cols,
-                           cudaStream_t stream)
+cudaError_t launch_mx_pair(const MxGemmParams &p, const MxSlots &sl, int cols, cudaStream_t stream)
 {
     int active = 0;
     cudaError_t e = active_pairs(active);
     if (e != cudaSuccess) return e;
     const unsigned pairs = (unsigned)std::min<int64_t>((int64_t)p.n_mblk * p.n_nblk, active);
-    if (rank_bucket_max == 0) return launch_pair<0>(p, sl, cols, pairs, stream);
-    if (rank_bucket_max <= 16) return launch_pair<16>(p, sl, cols, pairs, stream);
+    if (p.rank_bucket_max == 0) return launch_pair<0>(p, sl, cols, pairs, stream);
+    if (p.rank_bucket_max <= 16) return launch_pair<16>(p, sl, cols, pairs, stream);
     return launch_pair<64>(p, sl, cols, pairs, stream);
 }
 

@@ -3,30 +3,17 @@ valid adapter segment has the row, in every tile, every CTA of a cluster and eve
 named once get their own adapter as ever.
 
 The sums are of small integers, exact in fp32: results are compared bit for bit."""
-import ctypes
-
 import numpy as np
 import pytest
 import torch
 
 import segmented_rank_gemm_02_b200 as mlora
 from gpu_harness import DEVICE, free
+from mx_plan import planned
 
 pytestmark = pytest.mark.gpu
 
 SLOTS, RANK = 5, 8
-
-
-class _Plan(ctypes.Structure):
-    _fields_ = [("rows", ctypes.c_int32), ("cols", ctypes.c_int32), ("ksplit", ctypes.c_int32)]
-
-
-def planned(n_rows, d_in, d_out):
-    """The form that the library chooses for a product: (rows, columns of a tile, CTAs a tile)."""
-    fn = mlora.lib()._ZN5mlora12plan_mx_gemmEiii
-    fn.argtypes, fn.restype = [ctypes.c_int32] * 3, _Plan
-    p = fn(n_rows, d_in, d_out)
-    return p.rows, p.cols, p.ksplit
 
 
 def _case(n, n_tokens, d_in, d_out, run, seed):

@@ -1,0 +1,81 @@
+"""The 4-bit product in each of its forms, with adapters: the cases are chosen by the form that the
+library plans for them, which is checked.
+
+The operands are small integers whose sums stay below 2^24, exact in fp32, so an output is the
+64-bit result rounded once to its type: compared bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import segmented_rank_gemm_02_b200 as mlora
+from gpu_harness import DEVICE, free
+from mx_plan import planned
+
+pytestmark = pytest.mark.gpu
+
+DTYPES = [torch.float32, torch.bfloat16, torch.float16]
+
+
+def _ints(gen, *shape):
+    return torch.randint(-2, 3, shape, generator=gen, device=DEVICE).double()
+
+
+class _Case:
+    """A pool of `ranks` (slot a has rank ranks[a % len]), its adapters, and integer rows and weights."""
+
+    def __init__(self, n, d_in, d_out, n_slots, ranks, seed, r_max=None):
+        g = torch.Generator(device=DEVICE)
+        g.manual_seed(seed)
+        self.n, self.d_out, self.n_slots = n, d_out, n_slots
+        self.X, self.W = _ints(g, n, d_in), _ints(g, d_out, d_in)
+        self.X[:, ::32] = self.W[:, ::32] = 4.0    # the block's largest: a scale of 1
+        self.pool = mlora.Pool(d_in, d_out, n_slots, r_max or max(ranks))
+        self.A, self.B = [], []
+        for a in range(n_slots):
+            r = ranks[a % len(ranks)]
+            A, B = _ints(g, r, d_in), _ints(g, d_out, r)
+            A[torch.rand(A.shape, generator=g, device=DEVICE) > 8 / d_in] = 0
+            self.A.append(A), self.B.append(B)
+            self.pool.load_slot(a, r, float(r), A.bfloat16(), B.bfloat16())   # scale 1
+        self.Xb = self.X.bfloat16()
+        self.Xq, self.Wq = mlora.mx_quantize(self.Xb), mlora.mx_quantize(self.W.float())
+
+    def want(self, slot):
+        Y = self.X @ self.W.T
+        for a in range(self.n_slots):
+            at = torch.from_numpy(np.flatnonzero(slot == a)).to(DEVICE)
+            Y[at] += (self.X[at] @ self.A[a].T) @ self.B[a].T
+        assert Y.abs().max() < 60000    # fp16's range too
+        return Y
+
+    def check(self, segs, slot, dtypes=DTYPES):
+        want = self.want(slot)
+        for dtype in dtypes:
+            Y = torch.full((self.n, self.d_out), float("nan"), dtype=dtype, device=DEVICE)
+            mlora.mx_gemm_apply(self.pool, segs, self.Xb, self.Xq, self.Wq, Y)
+            assert torch.equal(Y, want.to(dtype))
+        assert self.pool.check() == 0
+
+
+def _slots(n, n_slots, runs, seed, base=0.15):
+    rng = np.random.default_rng(seed)
+    slot = rng.integers(0, n_slots, n).astype(np.int32)
+    slot[rng.random(n) < base] = -1
+    return np.sort(slot) if runs else slot
+
+
+def _segments(c, slot):
+    return mlora.DeviceSegments(mlora.build_segments(slot, c.pool), c.n, DEVICE)
+
+
+@pytest.mark.parametrize("n,d_in,d_out,form", [(100, 264, 136, (128, 128, 1)), (40, 8192, 136, (128, 128, 4)),
+                                               (1300, 520, 2056, (256, 256, 1)), (2600, 256, 4104, (256, 384, 1))])
+@pytest.mark.parametrize("r_max,ranks", [(8, (1, 3, 8)), (16, (16, 9)), (32, (32, 17, 8)), (64, (64, 33, 2))])
+def test_each_rank_bucket_in_each_form(n, d_in, d_out, form, r_max, ranks):
+    """Pools whose largest bucket is 8, 16, 32 and 64; rows standing together and scattered."""
+    assert planned(n, d_in, d_out) == form
+    c = _Case(n, d_in, d_out, 6, ranks, n + r_max, r_max)
+    for runs in (True, False):
+        slot = _slots(n, 6, runs, r_max)
+        c.check(_segments(c, slot), slot, [torch.float32, torch.bfloat16])
+    free()
