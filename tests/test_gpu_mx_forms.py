@@ -68,6 +68,21 @@ def _segments(c, slot):
     return mlora.DeviceSegments(mlora.build_segments(slot, c.pool), c.n, DEVICE)
 
 
+@pytest.mark.parametrize("n,d_in,d_out,n_slots,ranks,runs", [
+    (4608, 4096, 2048, 8, (64,), True),
+    (2560, 512, 1032, 12, (16,), False),
+    (1300, 1024, 2056, 70, (1, 8), False),       # more slots a row block than one ring stage holds
+    (2048, 256, 2048, 9, (5, 16, 24, 40, 64), False),
+    (2600, 264, 1032, 5, (32,), True),
+])
+def test_256_column_pair_tiles(n, d_in, d_out, n_slots, ranks, runs):
+    assert planned(n, d_in, d_out) == (256, 256, 1)
+    c = _Case(n, d_in, d_out, n_slots, ranks, n)
+    slot = _slots(n, n_slots, runs, n)
+    c.check(_segments(c, slot), slot)
+    free()
+
+
 @pytest.mark.parametrize("n,d_in,d_out,form", [(100, 264, 136, (128, 128, 1)), (40, 8192, 136, (128, 128, 4)),
                                                (1300, 520, 2056, (256, 256, 1)), (2600, 256, 4104, (256, 384, 1))])
 @pytest.mark.parametrize("r_max,ranks", [(8, (1, 3, 8)), (16, (16, 9)), (32, (32, 17, 8)), (64, (64, 33, 2))])
@@ -78,4 +93,53 @@ def test_each_rank_bucket_in_each_form(n, d_in, d_out, form, r_max, ranks):
     for runs in (True, False):
         slot = _slots(n, 6, runs, r_max)
         c.check(_segments(c, slot), slot, [torch.float32, torch.bfloat16])
+    free()
+
+
+@pytest.mark.parametrize("n,d_in,d_out,ksplit", [(4, 3584, 136, 2), (2, 3584, 64, 2), (60, 8192, 256, 4),
+                                                 (5, 8192, 128, 4), (128, 8192, 200, 4), (9, 14336, 64, 8)])
+@pytest.mark.parametrize("n_slots", [1, 3, 40])
+def test_adapters_divided_over_a_cluster(n, d_in, d_out, ksplit, n_slots):
+    """d_in split over 2, 4 and 8 CTAs, whose slots are every ksplit-th: fewer of them than CTAs, and more."""
+    assert planned(n, d_in, d_out) == (128, 128, ksplit)
+    c = _Case(n, d_in, d_out, n_slots, (8, 64, 16, 20), n + n_slots)
+    for base in (0.0, 0.5):
+        slot = _slots(n, n_slots, False, n_slots, base)
+        c.check(_segments(c, slot), slot)
+    free()
+
+
+def test_pair_tiles_with_a_list_of_rows_past_one_lookup():
+    """More grouped positions than the one-launch lookup of the pair form takes."""
+    n, d_in, d_out = 34000, 64, 1032
+    assert planned(n, d_in, d_out)[0] == 256
+    c = _Case(n, d_in, d_out, 9, (8, 16), 3)
+    for runs in (True, False):
+        slot = _slots(n, 9, runs, 5)
+        c.check(_segments(c, slot), slot, [torch.float32])
+    free()
+
+
+def _many_segments(n, run, n_slots, seed):
+    """Segments of `run` positions of shuffled rows, neighbours with equal slots among them."""
+    rng = np.random.default_rng(seed)
+    offsets = np.append(np.arange(0, n, run), n).astype(np.int32)
+    slots = rng.integers(-1, n_slots, offsets.size - 1).astype(np.int32)
+    rows = rng.permutation(n).astype(np.int32)
+    slot = np.empty(n, np.int32)
+    slot[rows] = np.repeat(slots, np.diff(offsets))
+    return {"offsets": offsets, "slots": slots, "token_indices": rows, "max_segment_rows": 1}, slot
+
+
+@pytest.mark.parametrize("n,run", [(4000, 2), (2048, 2), (36000, 5)])   # 2000, 1024, 7200 segments
+def test_more_segments_than_the_lookups_keep(n, run):
+    """Segment lists longer than the pair form's and the bf16 product's shared-memory tables."""
+    meta, slot = _many_segments(n, run, 7, n)
+    assert planned(n, 256, 1544)[0] == 256 and len(meta["slots"]) > 1023
+    c = _Case(n, 256, 1544, 7, (8, 12), n)
+    segs = mlora.DeviceSegments(meta, n, DEVICE)
+    c.check(segs, slot, [torch.float32])
+    Y = torch.full((n, 1544), float("nan"), dtype=torch.bfloat16, device=DEVICE)
+    mlora.base_gemm_apply(c.pool, segs, c.Xb, c.W.bfloat16(), Y)
+    assert c.pool.check() == 0 and torch.equal(Y, c.want(slot).bfloat16())
     free()
