@@ -657,8 +657,10 @@ def _weights_ptr(groups: RowGroups, w, index: int, what: str):
     import torch
     if w is None:
         return None
-    if w.dtype != torch.float32 or w.numel() != groups.n_tokens or not w.is_contiguous() or w.get_device() != index:
-        raise ValueError(f"{what} must be contiguous fp32 [n_rows, top_k] on the rows' device")
+    shape = tuple(w.shape)
+    if (w.dtype != torch.float32 or not w.is_contiguous() or w.get_device() != index
+            or shape not in ((groups.n_rows, groups.top_k), (groups.n_tokens,))):
+        raise ValueError(f"{what} must be contiguous fp32 [n_rows, top_k] (or flat) on the rows' device")
     return w.data_ptr()
 
 

@@ -1,0 +1,34 @@
+"""Operands that the binding of the 4-bit and grouped-row calls refuses (no GPU is needed)."""
+from types import SimpleNamespace
+
+import pytest
+import torch
+
+
+@pytest.fixture(scope="module")
+def mlora():
+    from segmented_rank_gemm_02_b200 import build
+    build.build()
+    import segmented_rank_gemm_02_b200 as m
+    m.lib()
+    return m
+
+
+def _groups(mlora, n, k):
+    return mlora.RowGroups(SimpleNamespace(handle=None, n_slots=3, device_index=-1), n, k, "cpu")
+
+
+def test_weights_of_another_shape_are_refused(mlora):
+    """As many weights in another arrangement would be read as other choices' weights."""
+    gr, Ys, dY = _groups(mlora, 6, 2), torch.zeros(12, 8), torch.zeros(6, 8)
+    for shape in ((2, 6), (12, 1), (1, 12), (3, 4), (6, 2, 1)):
+        w = torch.ones(shape)
+        with pytest.raises(ValueError, match="weights must be"):
+            mlora.combine_rows(gr, Ys, w)
+        with pytest.raises(ValueError, match="weights must be"):
+            mlora.combine_rows_backward(gr, dY, Ys, w)
+        with pytest.raises(ValueError, match="dweights must be"):
+            mlora.combine_rows_backward(gr, dY, Ys, None, dweights=w)
+    for shape in ((6, 2), (12,)):   # get as far as the device
+        with pytest.raises(ValueError, match="CUDA device"):
+            mlora.combine_rows(gr, Ys, torch.ones(shape))
