@@ -469,8 +469,8 @@ class MxMatrix:
             raise ValueError("codes and scales must be on one device")
         self._codes, self._scales = codes, scales
         self._index = codes.get_device()
-        self.struct = MxStruct(n_rows, n_cols, _ld(codes, "codes") if n_rows > 1 else row_bytes, _ptr(codes),
-                               _ptr(scales))
+        ld = _ld(codes, "codes")
+        self.struct = MxStruct(n_rows, n_cols, ld if n_rows > 1 else row_bytes, _ptr(codes), _ptr(scales))
 
     def _scale_shape(self):
         return ((self.n_rows + 127) // 128, 2 * ((self.n_cols + 255) // 256), 32, 4, 4)

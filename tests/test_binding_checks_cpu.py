@@ -32,3 +32,15 @@ def test_weights_of_another_shape_are_refused(mlora):
     for shape in ((6, 2), (12,)):   # get as far as the device
         with pytest.raises(ValueError, match="CUDA device"):
             mlora.combine_rows(gr, Ys, torch.ones(shape))
+
+
+@pytest.mark.parametrize("n", [1, 3])
+def test_codes_whose_bytes_are_apart_are_refused(mlora, n):
+    """A row's codes have to be consecutive, of a matrix of one row too."""
+    scales = torch.zeros(1, 2, 32, 4, 4, dtype=torch.uint8)
+    apart = torch.zeros(n, 64, dtype=torch.uint8)[:, ::2]
+    with pytest.raises(ValueError, match="codes must be"):
+        mlora.MxMatrix(n, 64, codes=apart, scales=scales)
+    with pytest.raises(ValueError, match="codes must be"):
+        mlora.MxMatrix(n, 64, codes=apart)
+    assert mlora.MxMatrix(n, 64, codes=apart.contiguous(), scales=scales).struct.ld == 32
