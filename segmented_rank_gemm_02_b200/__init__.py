@@ -458,9 +458,9 @@ class MxMatrix:
             return
         shape = self._scale_shape()
         if codes is None:
-            codes = torch.empty((n_rows, row_bytes), dtype=torch.uint8, device=scales.device)
+            codes = _empty(scales, (n_rows, row_bytes), torch.uint8, stream)
         if scales is None:
-            scales = torch.empty(shape, dtype=torch.uint8, device=codes.device)
+            scales = _empty(codes, shape, torch.uint8, stream)
         if codes.dtype != torch.uint8 or tuple(codes.shape) != (n_rows, row_bytes):
             raise ValueError(f"codes must be uint8 [{n_rows}, {row_bytes}]")
         if scales.dtype != torch.uint8 or tuple(scales.shape) != shape or not scales.is_contiguous():

@@ -44,3 +44,18 @@ def test_codes_whose_bytes_are_apart_are_refused(mlora, n):
     with pytest.raises(ValueError, match="codes must be"):
         mlora.MxMatrix(n, 64, codes=apart)
     assert mlora.MxMatrix(n, 64, codes=apart.contiguous(), scales=scales).struct.ld == 32
+
+
+def test_a_matrix_allocates_on_its_stream(mlora, monkeypatch):
+    """Whatever part of a matrix is allocated belongs to the stream that the matrix is for."""
+    seen = []
+
+    def empty(like, shape, dtype, stream):
+        seen.append(stream)
+        return torch.zeros(shape, dtype=dtype)
+
+    monkeypatch.setattr(mlora, "_empty", empty)
+    mlora.MxMatrix(3, 64, "cpu", stream=7)
+    mlora.MxMatrix(3, 64, codes=torch.zeros(3, 32, dtype=torch.uint8), stream=8)
+    mlora.MxMatrix(3, 64, scales=torch.zeros(1, 2, 32, 4, 4, dtype=torch.uint8), stream=9)
+    assert seen == [7, 8, 9]
