@@ -441,8 +441,8 @@ class MxMatrix:
     def __init__(self, n_rows: int, n_cols: int, device=None, codes=None, scales=None, stream=None, like=None):
         import torch
         n_rows, n_cols = int(n_rows), int(n_cols)
-        if n_rows < 0 or n_cols <= 0 or n_cols % 8 != 0:
-            raise ValueError("a 4-bit matrix has n_rows >= 0 and n_cols a positive multiple of 8")
+        if not 0 <= n_rows < 1 << 31 or not 0 < n_cols < 1 << 31 or n_cols % 8 != 0:
+            raise ValueError("a 4-bit matrix has 0 <= n_rows < 2^31 and n_cols a positive multiple of 8 below 2^31")
         row_bytes = (n_cols + 31) // 32 * 16
         self.n_rows, self.n_cols = n_rows, n_cols
         self._codes, self._scales = codes, scales
@@ -558,6 +558,8 @@ class RowGroups:
                  with_ranks: bool = True, like=None):
         import torch
         n = n_rows * top_k
+        if n > 1 << 30:
+            raise ValueError("at most 2^30 entries are grouped")
         S = min(pool.n_slots + 1, n)
         self.pool, self.n_rows, self.top_k, self.n_tokens, self._S = pool, n_rows, top_k, n, S
         # one allocation; the tensors are made when asked for

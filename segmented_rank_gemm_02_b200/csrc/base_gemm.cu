@@ -583,7 +583,7 @@ cudaError_t launch_row_map(const TileParams &p, int4 *row_info, cudaStream_t str
 
 cudaError_t launch_block_slots(const TileParams &p, int4 *row_info, int32_t *block_slots, cudaStream_t stream)
 {
-    const int n_mblk = (p.n_rows + PM - 1) / PM;
+    const int n_mblk = (int)(((int64_t)p.n_rows + PM - 1) / PM);
     if (n_mblk <= 0) return cudaSuccess;
     block_slots_kernel<<<n_mblk, PM, 0, stream>>>(p, row_info, block_slots);
     return cudaGetLastError();
@@ -594,7 +594,7 @@ constexpr int kSearchTokens = 32768;
 
 cudaError_t launch_row_blocks(const TileParams &p, int4 *row_info, int32_t *block_slots, cudaStream_t stream)
 {
-    const int n_mblk = (p.n_rows + PM - 1) / PM;
+    const int n_mblk = (int)(((int64_t)p.n_rows + PM - 1) / PM);
     if (n_mblk <= 0) return cudaSuccess;
     if (p.n_segments > 0 && p.n_tokens <= kSearchTokens) {
         row_blocks_kernel<<<n_mblk, kSearchThreads, 0, stream>>>(p, row_info, block_slots);

@@ -801,8 +801,8 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
     g.n_rows = Xq->n_rows;
     g.d_in = pool->d_in;
     g.d_out = pool->d_out;
-    g.n_mblk = (Xq->n_rows + plan.rows - 1) / plan.rows;
-    g.n_nblk = (pool->d_out + plan.cols - 1) / plan.cols;
+    g.n_mblk = (int32_t)(((int64_t)Xq->n_rows + plan.rows - 1) / plan.rows);
+    g.n_nblk = (int32_t)(((int64_t)pool->d_out + plan.cols - 1) / plan.cols);
     if (!lora) {
         const cudaError_t e = few ? mlora::launch_mx_tile(g, mlora::MxSegments{}, plan.ksplit, cs)
                                   : mlora::launch_mx_pair(g, mlora::MxSlots{}, plan.cols, cs);

@@ -1067,6 +1067,8 @@ cudaError_t launch_pair(const MxGemmParams &p, const MxSlots &sl, int cols, unsi
 
 }  // namespace
 
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
 {
     // Each form's time in us, as measured on a B200 with 148 SMs (shapes of 1 to 4096 rows, d_in
@@ -1074,8 +1076,8 @@ MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
     // for a split tile the exchange of its parts.  E.g. 256 x 4096 -> 4096: 8.4 us with one CTA a
     // tile, 9.9 with two, 10.8 on pairs; 512 x 4096 -> 14336: 32.5, 63, 18.9; one row of
     // 4096 -> 4096: 8.0 with one, 7.3 with two or four.
-    const int64_t nkb = (d_in + KB - 1) / KB;
-    const int64_t tiles = (int64_t)((n_rows + MR - 1) / MR) * ((d_out + MC - 1) / MC);
+    const int64_t nkb = ceil_div(d_in, KB);
+    const int64_t tiles = ceil_div(n_rows, MR) * ceil_div(d_out, MC);
     MxPlan plan{MR, MC, 1};
     double best = 1e30;
     for (int ks = 1; ks <= 8 && ks <= nkb; ks *= 2) {
@@ -1087,7 +1089,7 @@ MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
         }
     }
     for (int cols = 256; cols <= 384; cols += 128) {
-        const int64_t pairs = (int64_t)((n_rows + 2 * MR - 1) / (2 * MR)) * ((d_out + cols - 1) / cols);
+        const int64_t pairs = ceil_div(n_rows, 2 * MR) * ceil_div(d_out, cols);
         const double tile = cols == 256 ? 2.2 + 0.3125 * (double)nkb : 2.8 + 0.43 * (double)nkb;
         const double cost = 3.9 + (double)((pairs + 73) / 74) * tile;
         if (cost < best) {

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kQuantThreads, sizeof(T) == 2 ? 8 : 5) mx_quan
             c = e2m1x8(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv, f[4] * inv, f[5] * inv, f[6] * inv, f[7] * inv);
         }
         const int row = row0 + 32 * u;
-        if (row < q.n_rows && col < (q.n_cols + 31) / 32 * 32)
+        if (row < q.n_rows && col / 32 <= (q.n_cols - 1) / 32)   // the padding of the last block too
             *reinterpret_cast<uint32_t *>(q.codes + row * q.ld + col / 2) = c;
     }
     // 4 x 4 bytes, blocks x rows -> rows x blocks: lane u of each half stores row u's word
@@ -295,7 +295,7 @@ MxRows rows_of(const mlora_mx_matrix *Q)
     q.scales = static_cast<uint8_t *>(Q->scales);
     q.n_rows = Q->n_rows;
     q.n_cols = Q->n_cols;
-    q.chunks = (Q->n_cols + 255) / 256;
+    q.chunks = (int32_t)(((int64_t)Q->n_cols + 255) / 256);
     return q;
 }
 

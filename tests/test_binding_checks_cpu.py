@@ -59,3 +59,20 @@ def test_a_matrix_allocates_on_its_stream(mlora, monkeypatch):
     mlora.MxMatrix(3, 64, codes=torch.zeros(3, 32, dtype=torch.uint8), stream=8)
     mlora.MxMatrix(3, 64, scales=torch.zeros(1, 2, 32, 4, 4, dtype=torch.uint8), stream=9)
     assert seen == [7, 8, 9]
+
+
+def test_sizes_past_32_bits_are_refused(mlora):
+    """Sizes reach the library as 32-bit numbers: larger ones would arrive as others."""
+    codes, scales = torch.empty(0, dtype=torch.uint8), torch.empty(0, dtype=torch.uint8)
+    for n, d in ((1 << 31, 8), ((1 << 32) + 5, 8), (1, 1 << 31), (1, (1 << 32) + 8)):
+        with pytest.raises(ValueError, match="4-bit matrix has"):
+            mlora.MxMatrix(n, d, codes=codes, scales=scales)
+    for n, k in (((1 << 30) + 1, 1), ((1 << 32) + 5, 1), (1 << 16, (1 << 14) + 1)):
+        with pytest.raises(ValueError, match="entries"):
+            mlora.RowGroups(SimpleNamespace(n_slots=3), n, k, "meta")
+
+
+def test_plan_of_the_longest_matrices(mlora):
+    from mx_plan import planned
+    for n in ((1 << 31) - 1, (1 << 31) - 100, (1 << 31) - 257):
+        assert planned(n, 64, 64) == (256, 256, 1)

@@ -143,3 +143,30 @@ def test_more_segments_than_the_lookups_keep(n, run):
     mlora.base_gemm_apply(c.pool, segs, c.Xb, c.W.bfloat16(), Y)
     assert c.pool.check() == 0 and torch.equal(Y, c.want(slot).bfloat16())
     free()
+
+
+def test_quantize_the_longest_row():
+    """A row of 2^31 - 8 columns: padding and chunk counts that 32-bit sums would not hold."""
+    d = (1 << 31) - 8
+    g = torch.Generator(device=DEVICE)
+    g.manual_seed(1)
+    X = torch.zeros(1, d, dtype=torch.bfloat16, device=DEVICE)
+    spots = torch.tensor([0, 255, 256, 1 << 30, d - 257, d - 32, d - 25, d - 24, d - 9, d - 1], device=DEVICE)
+    X[0, spots] = torch.randn(spots.numel(), generator=g, device=DEVICE).bfloat16()
+    Q = mlora.mx_quantize(X)
+    for lo in (0, d - 24 - 256):     # the last block has 24 columns; a piece of whole blocks before it
+        piece = X[:, lo: lo + 280].contiguous()
+        part = mlora.mx_quantize(piece)
+        assert torch.equal(Q.codes[:, lo // 2: lo // 2 + 144], part.codes)
+        out = torch.empty(1, 280, dtype=torch.bfloat16, device=DEVICE)
+        mlora.mx_dequantize(part, out=out)
+        X[:, lo: lo + 280] = out
+    back = torch.zeros_like(X)
+    mlora.mx_dequantize(Q, out=back)
+    for lo in (0, d - 24 - 256):
+        assert torch.equal(back[:, lo: lo + 280], X[:, lo: lo + 280])
+    for at in ((1 << 30), d - 300):  # between them: what stands alone in its block, and zeros
+        block = back[0, at: at + 20].float()
+        assert torch.equal(block != 0, X[0, at: at + 20] != 0)
+    del X, Q, back
+    free()
