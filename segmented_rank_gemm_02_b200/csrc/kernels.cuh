@@ -256,11 +256,12 @@ struct MxSlots {
 };
 
 // Tiles of a form: rows and columns of Y per tile (128 x 128, the few-rows form; 256 x 256 or
-// 256 x 384, the many-rows one) and CTAs per tile of the few-rows form.
+// 256 x 384, the many-rows one) and CTAs per tile of the few-rows form.  n_tokens: grouped positions
+// (0 without LoRA).
 struct MxPlan {
     int rows, cols, ksplit;
 };
-MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out);
+MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out, int n_tokens);
 
 // Y = X W^T (+ the slots' low-rank products if p.rank_bucket_max > 0).
 // Both launch with programmatic dependent launch: they read nothing before the kernels that the

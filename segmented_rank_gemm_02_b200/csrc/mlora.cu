@@ -784,7 +784,7 @@ mlora_status mlora_mx_gemm_apply(mlora_pool *pool, const mlora_segments *segs, c
     if (st != MLORA_OK) return st;
     cudaStream_t cs = static_cast<cudaStream_t>(stream);
 
-    const mlora::MxPlan plan = mlora::plan_mx_gemm(Xq->n_rows, pool->d_in, pool->d_out);
+    const mlora::MxPlan plan = mlora::plan_mx_gemm(Xq->n_rows, pool->d_in, pool->d_out, lora ? segs->n_tokens : 0);
     const bool few = plan.rows == mlora::kMxTileRows;   // the few-rows form
     const int b_cols = plan.cols == 384 ? 96 : 128;     // W rows (B columns) a CTA loads at a time
     mlora::MxGemmParams g{};

@@ -1069,7 +1069,13 @@ cudaError_t launch_pair(const MxGemmParams &p, const MxSlots &sl, int cols, unsi
 
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
+// With adapters every CTA of the few-rows form walks the whole list of grouped positions, so its time
+// grows with their square; the many-rows form has them looked up once.  Whole calls with adapters, few-rows
+// against pair tiles, in us: 64 -> 64, 8192 rows 26 / 26, 16384 34 / 30, 60000 245 / 61; 512 -> 128
+// 28 / 28, 36 / 32, 280 / 90; 4096 -> 128 38 / 40, 71 / 61, 382 / 167.
+constexpr int kTileTokens = 8192;
+
+MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out, int n_tokens)
 {
     // Each form's time in us, as measured on a B200 with 148 SMs (shapes of 1 to 4096 rows, d_in
     // 1024 to 14336): waves of resident CTAs or pairs times (what a tile costs + its K blocks), and
@@ -1080,7 +1086,7 @@ MxPlan plan_mx_gemm(int n_rows, int d_in, int d_out)
     const int64_t tiles = ceil_div(n_rows, MR) * ceil_div(d_out, MC);
     MxPlan plan{MR, MC, 1};
     double best = 1e30;
-    for (int ks = 1; ks <= 8 && ks <= nkb; ks *= 2) {
+    for (int ks = 1; ks <= 8 && ks <= nkb && n_tokens <= kTileTokens; ks *= 2) {
         const double exchange = ks > 1 ? 1.0 + 0.5 * ks + 0.02 * std::min(n_rows, MR) : 0.0;
         const double cost = (double)((tiles * ks + 147) / 148) * (3.1 + 0.31 * (double)((nkb + ks - 1) / ks) + exchange);
         if (cost < best) {

@@ -76,3 +76,14 @@ def test_plan_of_the_longest_matrices(mlora):
     from mx_plan import planned
     for n in ((1 << 31) - 1, (1 << 31) - 100, (1 << 31) - 257):
         assert planned(n, 64, 64) == (256, 256, 1)
+
+
+def test_plan_of_a_long_list_of_rows(mlora):
+    """With adapters the few-rows form's time grows with the square of the list: it is left to short ones,
+    few rows named by a long list included."""
+    from mx_plan import planned
+    for n, d_in, d_out in ((60000, 512, 128), (1 << 24, 8, 8), (16384, 64, 64), (8, 4096, 128)):
+        if n < 1 << 24:
+            assert planned(n, d_in, d_out)[0] == 128
+        assert planned(n, d_in, d_out, max(n, 60000))[0] == 256
+    assert planned(256, 4096, 4096, 256) == planned(256, 4096, 4096)

@@ -62,7 +62,7 @@ CASES = [
 
 @pytest.mark.parametrize("n,n_tokens,d_in,d_out,run,form", CASES)
 def test_lowest_position_has_the_row(n, n_tokens, d_in, d_out, run, form):
-    assert planned(n, d_in, d_out) == form
+    assert planned(n, d_in, d_out, n_tokens) == form
     pool, segs, X, W, want = _case(n, n_tokens, d_in, d_out, run, n + n_tokens)
     Xq, Wq = mlora.mx_quantize(X), mlora.mx_quantize(W)
     for _ in range(4):

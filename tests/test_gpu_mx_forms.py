@@ -76,7 +76,7 @@ def _segments(c, slot):
     (2600, 264, 1032, 5, (32,), True),
 ])
 def test_256_column_pair_tiles(n, d_in, d_out, n_slots, ranks, runs):
-    assert planned(n, d_in, d_out) == (256, 256, 1)
+    assert planned(n, d_in, d_out, n) == (256, 256, 1)
     c = _Case(n, d_in, d_out, n_slots, ranks, n)
     slot = _slots(n, n_slots, runs, n)
     c.check(_segments(c, slot), slot)
@@ -88,7 +88,7 @@ def test_256_column_pair_tiles(n, d_in, d_out, n_slots, ranks, runs):
 @pytest.mark.parametrize("r_max,ranks", [(8, (1, 3, 8)), (16, (16, 9)), (32, (32, 17, 8)), (64, (64, 33, 2))])
 def test_each_rank_bucket_in_each_form(n, d_in, d_out, form, r_max, ranks):
     """Pools whose largest bucket is 8, 16, 32 and 64; rows standing together and scattered."""
-    assert planned(n, d_in, d_out) == form
+    assert planned(n, d_in, d_out, n) == form
     c = _Case(n, d_in, d_out, 6, ranks, n + r_max, r_max)
     for runs in (True, False):
         slot = _slots(n, 6, runs, r_max)
@@ -101,7 +101,7 @@ def test_each_rank_bucket_in_each_form(n, d_in, d_out, form, r_max, ranks):
 @pytest.mark.parametrize("n_slots", [1, 3, 40])
 def test_adapters_divided_over_a_cluster(n, d_in, d_out, ksplit, n_slots):
     """d_in split over 2, 4 and 8 CTAs, whose slots are every ksplit-th: fewer of them than CTAs, and more."""
-    assert planned(n, d_in, d_out) == (128, 128, ksplit)
+    assert planned(n, d_in, d_out, n) == (128, 128, ksplit)
     c = _Case(n, d_in, d_out, n_slots, (8, 64, 16, 20), n + n_slots)
     for base in (0.0, 0.5):
         slot = _slots(n, n_slots, False, n_slots, base)
@@ -112,11 +112,20 @@ def test_adapters_divided_over_a_cluster(n, d_in, d_out, ksplit, n_slots):
 def test_pair_tiles_with_a_list_of_rows_past_one_lookup():
     """More grouped positions than the one-launch lookup of the pair form takes."""
     n, d_in, d_out = 34000, 64, 1032
-    assert planned(n, d_in, d_out)[0] == 256
+    assert planned(n, d_in, d_out, n)[0] == 256
     c = _Case(n, d_in, d_out, 9, (8, 16), 3)
     for runs in (True, False):
         slot = _slots(n, 9, runs, 5)
         c.check(_segments(c, slot), slot, [torch.float32])
+    free()
+
+
+@pytest.mark.parametrize("n,d_in,d_out", [(8192, 64, 64), (8193, 64, 64), (16400, 512, 128), (40000, 256, 64)])
+def test_a_long_list_of_rows_leaves_the_few_rows_form(n, d_in, d_out):
+    assert planned(n, d_in, d_out)[0] == 128 and planned(n, d_in, d_out, n)[0] == (128 if n <= 8192 else 256)
+    c = _Case(n, d_in, d_out, 7, (8, 16), n)
+    slot = _slots(n, 7, False, 2)
+    c.check(_segments(c, slot), slot, [torch.float32, torch.bfloat16])
     free()
 
 
@@ -135,7 +144,7 @@ def _many_segments(n, run, n_slots, seed):
 def test_more_segments_than_the_lookups_keep(n, run):
     """Segment lists longer than the pair form's and the bf16 product's shared-memory tables."""
     meta, slot = _many_segments(n, run, 7, n)
-    assert planned(n, 256, 1544)[0] == 256 and len(meta["slots"]) > 1023
+    assert planned(n, 256, 1544, n)[0] == 256 and len(meta["slots"]) > 1023
     c = _Case(n, 256, 1544, 7, (8, 12), n)
     segs = mlora.DeviceSegments(meta, n, DEVICE)
     c.check(segs, slot, [torch.float32])
