@@ -304,7 +304,7 @@ int64_t mlora_mx_scale_bytes(int32_t n_rows, int32_t n_cols);
  * Quantise X (device, bf16, fp16 or fp32 as x_dtype says, [Q->n_rows, Q->n_cols], row
  * stride ldx elements, rows and strides of whole 16-byte vectors) into Q, on the current
  * device: activations before a 4-bit projection, or weights once when they are loaded.
- * MLORA_ERR_UNSUPPORTED if n_cols is no multiple of 8.
+ * Q's memory must not overlap X.  MLORA_ERR_UNSUPPORTED if n_cols is no multiple of 8.
  */
 mlora_status mlora_mx_quantize(const void *X, int32_t x_dtype, int64_t ldx, const mlora_mx_matrix *Q, void *stream);
 
@@ -323,7 +323,7 @@ mlora_status mlora_mx_dequantize(const mlora_mx_matrix *Q, void *X, int32_t x_dt
  * activations X from before the quantisation (bf16 [n_rows, d_in], row stride ldx), as
  * mlora_base_gemm_apply does, and the sum is rounded once to y_dtype (MLORA_DTYPE_BF16,
  * _FP16 or _FP32).  Y [n_rows, d_out], row stride ldy, is written for every row and never
- * read.  Xq is the caller's, so that projections that share X (q/k/v, gate/up) quantise it
+ * read; it must not overlap an input.  Xq is the caller's, so that projections that share X (q/k/v, gate/up) quantise it
  * once.  segs may be NULL: base projection only, for a module without adapters; X is then
  * not read and may be NULL.  Errors, rejected segments and the workspace as
  * mlora_base_gemm_apply; also MLORA_ERR_INVALID_ARG where a matrix does not match the
@@ -451,8 +451,8 @@ mlora_status mlora_group_rows(mlora_pool *pool, const int32_t *row_slots, int32_
  * The rows in grouped order: Xs[positions[t * top_k + j], :] = X[t, :].  X: device
  * [n_rows, d] and Xs: device [n_tokens, d], both of `dtype` (MLORA_DTYPE_BF16, _FP16 or
  * _FP32), row strides ldx and ldxs elements; rows and strides are whole 16-byte vectors
- * (MLORA_ERR_UNSUPPORTED for a d that is not) and 16-byte aligned.  Rows of Xs that no
- * position names are left as they were; a position of -1 is skipped, any other outside
+ * (MLORA_ERR_UNSUPPORTED for a d that is not) and 16-byte aligned.  Xs must not overlap X.
+ * Rows of Xs that no position names are left as they were; a position of -1 is skipped, any other outside
  * [0, n_tokens) is skipped and flagged MLORA_FLAG_BAD_ROW in the pool.  The gradient of X is
  * mlora_combine_rows of the gradient of Xs, without weights.
  */

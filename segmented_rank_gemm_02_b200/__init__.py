@@ -525,7 +525,8 @@ def mx_dequantize(Q: MxMatrix, out=None, dtype=None, stream=None):
 def mx_gemm_apply(pool: Pool, segs: Optional["DeviceSegments"], X, Xq: MxMatrix, W: MxMatrix, Y, stream=None) -> None:
     """Y = round(Xq W^T + s (X A^T) B^T) for adapter rows, round(Xq W^T) for the others, in one pass
     (mlora_mx_gemm_apply).  Xq [n_rows, d_in] and W [d_out, d_in] 4-bit, X the bf16 activations that
-    Xq was quantised from (not read, and may be None, if segs is None), Y bf16, fp16 or fp32."""
+    Xq was quantised from (not read, and may be None, if segs is None), Y bf16, fp16 or fp32.
+    Nothing is recorded for autograd, and the product has no gradient here."""
     n, index = Xq.n_rows, Y.get_device()
     if tuple(Y.shape) != (n, pool.d_out):
         raise ValueError("Y must be [rows of Xq, d_out]")
@@ -626,7 +627,8 @@ def group_rows(pool: Pool, row_slots, out: Optional[RowGroups] = None, max_segme
     """Sort rows by adapter slot on the device (mlora_group_rows).  row_slots: int32 [n_rows] or
     [n_rows, top_k], contiguous, -1 = base model; which of the two decides what the result is as
     segments (see RowGroups).  `out` reuses a RowGroups of the same sizes (a
-    captured graph's).  max_segment_rows: the hint of mlora_segments, if the caller knows one;
+    captured graph's).  max_segment_rows: the hint of mlora_segments, if the caller knows one (1 for
+    a decode batch used with its own rows, which spares it the launches for long segments);
     with_ranks: see RowGroups (both only without `out`)."""
     import torch
     shape = row_slots.shape
@@ -668,7 +670,9 @@ def _weights_ptr(groups: RowGroups, w, index: int, what: str):
 
 def gather_rows(groups: RowGroups, X, Xs=None, stream=None):
     """Xs[positions[t, j]] = X[t]: the rows in grouped order (mlora_gather_rows).  The gradient of X
-    is combine_rows(groups, dXs)."""
+    is combine_rows(groups, dXs); nothing is recorded for autograd.  Entries whose slot is not the
+    pool's have no row: as many at the end of Xs, from offsets[-1] on, are left as they were, that
+    is uninitialised in a new Xs."""
     code, d, n, index = _float_code(X, "X"), X.shape[-1], groups.n_tokens, groups._index
     ldx = _rows_of(X, groups.n_rows, d, X.dtype, index, "X")
     if Xs is None:
@@ -681,7 +685,8 @@ def gather_rows(groups: RowGroups, X, Xs=None, stream=None):
 
 
 def combine_rows(groups: RowGroups, Ys, weights=None, Y=None, stream=None):
-    """Y[t] = sum_j weights[t, j] Ys[positions[t, j]] (mlora_combine_rows); weights fp32 or None (ones)."""
+    """Y[t] = sum_j weights[t, j] Ys[positions[t, j]] (mlora_combine_rows); weights fp32 or None (ones).
+    Nothing is recorded for autograd: the gradients are combine_rows_backward."""
     code, d, n, index = _float_code(Ys, "Ys"), Ys.shape[-1], groups.n_tokens, groups._index
     ldys = _rows_of(Ys, n, d, Ys.dtype, index, "Ys")
     w = _weights_ptr(groups, weights, index, "weights")
@@ -696,7 +701,9 @@ def combine_rows(groups: RowGroups, Ys, weights=None, Y=None, stream=None):
 
 def combine_rows_backward(groups: RowGroups, dY, Ys, weights=None, dYs=None, dweights=None, stream=None):
     """(dYs, dweights) of combine_rows from dY (mlora_combine_rows_backward).  Without weights only dYs
-    is computed (dweights is None, Ys may be None) unless a dweights tensor is given."""
+    is computed (dweights is None, Ys may be None) unless a dweights tensor is given.  Rows of dYs from
+    groups.offsets[-1] on (there are some only where a slot was not the pool's) are left as they were,
+    that is uninitialised in a new dYs: leave them out of sums over rows, or give a dYs of zeros."""
     import torch
     code, d, n, index = _float_code(dY, "dY"), dY.shape[-1], groups.n_tokens, groups._index
     lddy = _rows_of(dY, groups.n_rows, d, dY.dtype, index, "dY")

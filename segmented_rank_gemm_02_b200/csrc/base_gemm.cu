@@ -8,9 +8,10 @@
 //
 // Order of work.  The shrink H = X A_a^T is the library's segmented shrink (the
 // decode-shaped kernel, and the tensor-memory kernel for long segments) into an fp32
-// workspace in grouped order.  row_map_kernel then gives each row its grouped
+// workspace in grouped order.  Before it, row_blocks_kernel gives each row its grouped
 // position, slot, scale and rank (rows outside every valid segment keep position -1:
-// base only), and block_slots_kernel lists the distinct slots of each 256-row block.
+// base only) and lists the distinct slots of each 256-row block; for long lists of
+// grouped positions row_map_kernel and block_slots_kernel do so in two launches.
 // Last, the persistent GEMM below.
 //
 // GEMM tile: 256 rows x 256 columns of Y, computed by a pair of CTAs (a cluster of

@@ -11,8 +11,9 @@
 //   backward  dYs[positions[t, j]] = w[t, j] dY[t],  dw[t, j] = <dY[t], Ys[positions[t, j]]>
 //
 // gather's own gradient is combine without weights; combine's without weights is gather.
-// The last three read and write every row once and are bound by HBM; sums are fp32, one
-// rounding at the end.  No atomics, so results do not vary from run to run.
+// The last three are bound by HBM: rows are read and written once, but for backward, which
+// reads dY once for every four choices of a row.  Sums are fp32, one rounding at the end.  No
+// atomics, so results do not vary from run to run.
 #include "mlora.h"
 
 #include <algorithm>
