@@ -138,10 +138,20 @@ def _check(status: int, what: str) -> None:
         raise MloraError(status, what)
 
 
+_current_device = _raw_stream = None   # torch's, looked up once: a small call is mostly such look-ups
+
+
+def _look_up() -> None:
+    global _current_device, _raw_stream
+    if _current_device is None:
+        import torch
+        _current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+
+
 def _stream_ptr(stream) -> Optional[int]:
-    import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
+        _look_up()
+        return _raw_stream(_current_device())
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -401,15 +411,9 @@ def _float_code(t, what: str) -> int:
     return code
 
 
-_current_device = _raw_stream = None   # torch's, looked up once: a small call is mostly such look-ups
-
-
 def _call(fn, what: str, device: int, stream, *args) -> None:
     """fn(*args, stream) with `device` current, on its current stream unless one is given."""
-    global _current_device, _raw_stream
-    if _current_device is None:
-        import torch
-        _current_device, _raw_stream = torch.cuda.current_device, torch._C._cuda_getCurrentRawStream
+    _look_up()
     if device < 0:
         raise ValueError("the tensors must be on a CUDA device")
     if device != _current_device():
